@@ -178,7 +178,9 @@ def prepare(case, seed):
         at = torch.arange(cols, device="cuda")[None, :] < hv[:, None]
         table[at] = ids[: sum(have)]
         st.update(ctx=_i32(ctx), new=_i32(new), table=table, free=ids[sum(have):].contiguous(),
-                  num_pages=num, page=P, max_tokens=sum(new) + 5)
+                  num_pages=num, page=P, max_tokens=sum(new) + 5,
+                  bufs=tuple(torch.empty(n, dtype=torch.int32, device="cuda") for n in
+                             (case["B"] + 1, sum(new) + 5, sum(new) + 5, 2)))
         return st
     if op == "append":
         N, P = case["N"], case["page"]
@@ -342,7 +344,7 @@ def run(st):
     if op == "plan":
         cu, slots, pos, counts = b.page_plan(st["ctx"], st["new"], st["free"], st["table"],
                                              page_size=st["page"], num_pages=st["num_pages"],
-                                             max_tokens=st["max_tokens"])
+                                             max_tokens=st["max_tokens"], out=st["bufs"])
         return {"cu_new": cu, "slot_map": slots, "positions": pos, "counts": counts,
                 "block_table": st["table"]}
     if op == "append":
