@@ -450,10 +450,145 @@ mla_status_t mla_attn_oproj_fp8(const mla_bf16* q_nope, const mla_bf16* q_pe,
                                 mla_bf16* out, mla_stream_t stream);
 
 /*
+ * ------------------------------------------------------------ paged latent cache
+ * Serving steps keep, per layer, one row of 576 bf16 for every cached token:
+ * its KV latent c_kv (512, kv_lora_rank) and its rotated rotary key (64,
+ * shared by all heads) -- config.json on page "Kimi K2 · Block input". The
+ * pages print no cache; the library lays it out as
+ *   cache [num_pages, page_size, 576] bf16, pages page_stride elements apart
+ *         (page_stride >= page_size * 576 and a multiple of 8, so that the
+ *         pages of several layers can be interleaved);
+ *   block_table [B, max_pages] int32: the page of the tokens k * page_size ..
+ *         of request b, k < max_pages; entries outside [0, num_pages) name no
+ *         page;
+ *   slot  page * page_size + row, the index of one cached token.
+ * page_size is 16, 32, 64 or 128; num_pages * page_size <= 2^31 - 1.
+ * int32 arrays are 4-byte aligned, cache and bf16 tensors 16-byte aligned.
+ * Lengths are read on the device, so they are made safe rather than rejected:
+ * negative ones count as 0, and no access leaves the arrays whatever they hold.
+ */
+#define MLA_CACHE_DIM 576 /* MLA_KV_RANK + MLA_QK_ROPE_DIM */
+
+/*
+ * Block tables and slot maps of one step, on the GPU: request b, with
+ * context_len[b] tokens cached, adds new_len[b].
+ *   context_len, new_len  [B] int32
+ *   free_pages   [n_free] int32, pages to take from, in order (NULL if n_free
+ *                is 0); the list itself is not changed: the caller drops the
+ *                first counts[1] entries
+ *   node_depth   [max_tokens] int32 or NULL: depth of every new token below its
+ *                request's last cached token's successor (drafted trees)
+ *   block_table  [B, max_pages]: the request's ceil(context / page_size) first
+ *                entries are read, the entries of its new pages are written
+ *                (-1 where free_pages ran out), the others are left as they are
+ *   cu_new       [B + 1]: first new token of every request, then their sum
+ *   slot_map     [max_tokens]: slot of every new token, requests in order; -1
+ *                for a token without a page and behind the last token
+ *   positions    [max_tokens]: context_len[b] + i of request b's i-th new token
+ *                (+ node_depth of the token instead of i, when given); 0 behind
+ *                the last token
+ *   counts       [2]: new tokens, new pages asked for (more than n_free: the
+ *                list ran out). Sums saturate at 2^31 - 1.
+ *   B 1..65535, max_tokens 1..2^30, max_pages 1..2^31 - 1, n_free >= 0
+ * Tokens past max_tokens are not planned (cu_new and counts still count them).
+ */
+mla_status_t mla_page_plan(const int32_t* context_len, const int32_t* new_len, int B,
+                           const int32_t* free_pages, int n_free, const int32_t* node_depth,
+                           int num_pages, int page_size, int32_t* block_table, int max_pages,
+                           int32_t* cu_new, int32_t* slot_map, int32_t* positions,
+                           int max_tokens, int32_t* counts, mla_stream_t stream);
+
+/*
+ * Writes the step's tokens into the cache:
+ *   c_kv       [N, 512] bf16, k_pe [N, 64] bf16 (rotary key)
+ *   positions  [N] int32, used with rope only (then required)
+ *   rope       host pointer: k_pe is rotated at positions as in
+ *              mla_attn_prefill_rope; NULL: stored as it is
+ *   slot_map   [N] int32; a token whose slot lies outside [0, num_pages *
+ *              page_size) is skipped. Two tokens of one call may not share a
+ *              slot (its row would mix the two).
+ *   N          1 .. 2^31 - 129
+ */
+mla_status_t mla_cache_append(const mla_bf16* c_kv, const mla_bf16* k_pe,
+                              const int32_t* positions, const mla_yarn_rope_t* rope,
+                              const int32_t* slot_map, int64_t N, mla_bf16* cache, int num_pages,
+                              int page_size, int64_t page_stride, mla_stream_t stream);
+
+/*
+ * Workspace bytes of mla_attn_tree: the status word, the schedule (48 bytes a
+ * request), queries and outputs in latent form (N * 64 * (576 + 512) * 2) and
+ * 38 MiB of partial results. Returns 0 for B or N out of range.
+ */
+size_t mla_attn_tree_workspace_bytes(int B, int64_t N);
+
+/*
+ * Attention of a step's tokens over the paged cache: single tokens, chains and
+ * trees of drafted tokens. Rows cu_new[b] .. cu_new[b+1] - 1 of q are request
+ * b's nodes; their own cache rows follow its context_len[b] cached tokens and
+ * are in the cache already (mla_cache_append). Node i sees every cached token
+ * j < context_len[b] and those nodes d of its request that its mask row names:
+ *   s = softmax_scale * (q_nope . k_nope + q_pe . k_pe), softmax over the
+ *   visible tokens in fp32, out[n, h * 128 + e] = sum p v[.., e],
+ *   k_nope, v as mla_kv_up_proj gives them from W_kv_b (they are never formed:
+ *   W_kv_b is multiplied into the queries and into the result).
+ *   q_nope [N, 64, 128], q_pe [N, 64, 64] bf16, W_kv_b [16384, 512] bf16
+ *   positions  [N] int32, used with rope only (then required)
+ *   rope       host pointer: q_pe is rotated at positions; NULL: q_pe is
+ *              rotated already
+ *   tree_mask  [N, mask_words] 32-bit words: bit d % 32 of word d / 32 of row n
+ *              says whether row n sees node d of its request (nodes without a
+ *              bit are not seen); NULL: node i sees nodes 0 .. i
+ *   out        [N, 8192] bf16 (merged heads, what mla_o_proj and mla_o_proj_w4
+ *              read). A row that sees nothing is zeros; rows behind
+ *              cu_new[B] are left as they are.
+ *   B 1..65535, N 1 .. 2^24, max_pages >= 1, mask_words >= 1 with a mask
+ *   workspace  mla_attn_tree_workspace_bytes(B, N) bytes; not to be shared by
+ *              calls that can overlap.
+ * A visible token whose table entry names no page is taken as not visible.
+ * Cache rows that no node of the request sees may hold anything (NaN
+ * included); rows that some node sees must be finite.
+ */
+mla_status_t mla_attn_tree(const mla_bf16* q_nope, const mla_bf16* q_pe, const mla_bf16* W_kv_b,
+                           const int32_t* positions, const mla_yarn_rope_t* rope,
+                           const mla_bf16* cache, int num_pages, int page_size,
+                           int64_t page_stride, const int32_t* block_table, int max_pages,
+                           const int32_t* context_len, const int32_t* cu_new,
+                           const uint32_t* tree_mask, int mask_words, int B, int64_t N,
+                           float softmax_scale, void* workspace, size_t workspace_bytes,
+                           mla_bf16* out, mla_stream_t stream);
+
+/*
+ * ------------------------------------------------------------ 4-bit o_proj
+ * o_proj for the few rows of a serving step, where reading W_o bounds it:
+ *   out[m, n] = sum_g W_scale[n, g] * sum_{k in group g} (code[n, k] - 8) * attn[m, k]
+ * with codes 0..15, two per byte (feature 2i in the low nibble of byte i, 2i+1
+ * in the high one), groups of 32, 64 or 128 consecutive features and one bf16
+ * scale per row and group. fp32 accumulation, rounded once.
+ */
+
+/*
+ * W_o [7168, 8192] bf16 -> W_q [7168, 4096] codes, W_scale [7168, 8192 / group]
+ * bf16: scale = bf16(amax / 7) of the group (1 for a group of zeros), code = 8 +
+ * the integer nearest to w / scale (fp32 quotient, ties to even), clamped to
+ * -8 .. 7. W must be finite. Done once, like loading a checkpoint.
+ */
+mla_status_t mla_quantize_weight_w4(const mla_bf16* W, int group, uint8_t* W_q, mla_bf16* W_scale,
+                                    mla_stream_t stream);
+
+/*
+ *   attn [M, 8192] bf16, W_q and W_scale as above, group 32, 64 or 128 (else
+ *   MLA_ERR_SHAPE), out [M, 7168] bf16, M 1 .. 2^20. All pointers 16-byte
+ *   aligned. Meant for M up to about 128; mla_o_proj is the faster product for
+ *   many rows.
+ */
+mla_status_t mla_o_proj_w4(const mla_bf16* attn, const uint8_t* W_q, const mla_bf16* W_scale,
+                           int group, int64_t M, mla_bf16* out, mla_stream_t stream);
+
+/*
  * Outcome of the last call that used `workspace` (a workspace given to
  * mla_attn_prefill, mla_attn_oproj, mla_attn_oproj_varlen,
- * mla_attn_prefill_rope, mla_attn_oproj_rope, mla_attn_oproj_latent or
- * mla_attn_oproj_fp8; that call
+ * mla_attn_prefill_rope, mla_attn_oproj_rope, mla_attn_oproj_latent,
+ * mla_attn_oproj_fp8 or mla_attn_tree; that call
  * must have been enqueued on `stream` or be complete). Synchronises `stream`, then reads the call's status word.
  * Returns MLA_ERR_TIMEOUT if one of that call's kernels gave up on a bounded
  * wait, MLA_ERR_CUDA if the stream reports an error, MLA_ERR_INVALID_ARG for

@@ -6,6 +6,7 @@ is no fallback: if the library is missing or fails to load, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -93,6 +94,18 @@ _SIGNATURES = {
     "mla_attn_oproj_fp8": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int64,
                                           ctypes.c_int, ctypes.c_int, ctypes.c_float, _VP, _VP,
                                           _VP, ctypes.c_size_t, _VP, _VP]),
+    "mla_page_plan": (ctypes.c_int, [_VP, _VP, ctypes.c_int, _VP, ctypes.c_int, _VP, ctypes.c_int,
+                                     ctypes.c_int, _VP, ctypes.c_int, _VP, _VP, _VP,
+                                     ctypes.c_int, _VP, _VP]),
+    "mla_cache_append": (ctypes.c_int, [_VP, _VP, _VP, _ROPE_P, _VP, ctypes.c_int64, _VP,
+                                        ctypes.c_int, ctypes.c_int, ctypes.c_int64, _VP]),
+    "mla_attn_tree_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int64]),
+    "mla_attn_tree": (ctypes.c_int, [_VP, _VP, _VP, _VP, _ROPE_P, _VP, ctypes.c_int, ctypes.c_int,
+                                     ctypes.c_int64, _VP, ctypes.c_int, _VP, _VP, _VP,
+                                     ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
+                                     _VP, ctypes.c_size_t, _VP, _VP]),
+    "mla_quantize_weight_w4": (ctypes.c_int, [_VP, ctypes.c_int, _VP, _VP, _VP]),
+    "mla_o_proj_w4": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int, ctypes.c_int64, _VP, _VP]),
     "mla_last_device_status": (ctypes.c_int, [_VP, _VP, ctypes.POINTER(ctypes.c_uint32)]),
     "mla_device_status": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint32)]),
     "mla_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -561,6 +574,239 @@ def attn_oproj_fp8(q_nope, q_pe, k_nope, k_pe, v, W_q, W_scale, mask=None, softm
                                 _ptr(mask), mask_ld, B, T, scale, _ptr(W_q), _ptr(W_scale),
                                 _ptr(workspace), ws_bytes, _ptr(out), _stream_handle(stream))
     _check("mla_attn_oproj_fp8", st)
+    return out
+
+
+# ------------------------------------------------------------------ serving steps
+CACHE_DIM = KV_RANK + DR       # MLA_CACHE_DIM: one cached token, latent then rotary key
+PAGE_SIZES = (16, 32, 64, 128)
+W4_GROUPS = (32, 64, 128)
+
+
+@contextlib.contextmanager
+def _entered(dev, stream):
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield int(torch.cuda.current_stream().cuda_stream)
+        else:
+            with torch.cuda.stream(stream):
+                yield int(stream.cuda_stream)
+
+
+class _Here:
+    """The usual call: tensors on the current device, its current stream."""
+
+    def __enter__(self):
+        return int(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _launching(dev, stream):
+    """Context in which a call on ``dev``'s tensors runs: that device current,
+    and ``stream`` too when one is given, so that what the call allocates
+    belongs to the stream its kernels use. Yields the stream handle."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return _HERE
+    return _entered(dev, stream)
+
+
+def _on(dev, t, dtype, shape, name):
+    """_req_t, and the tensor lies on ``dev``."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _cache_pages(cache, dev):
+    """(pages, page size, page stride in elements) of a [pages, page_size, 576]
+    cache whose rows are dense (the pages may lie apart)."""
+    if cache.dtype != torch.bfloat16:
+        raise TypeError(f"cache must be bf16, got {cache.dtype}")
+    if cache.device != dev:
+        raise ValueError(f"cache must be on {dev}, got {cache.device}")
+    if cache.dim() != 3 or cache.shape[2] != CACHE_DIM:
+        raise ValueError(f"cache must be [pages, page_size, {CACHE_DIM}], got {tuple(cache.shape)}")
+    n, page, _ = cache.shape
+    if page not in PAGE_SIZES:
+        raise ValueError(f"page_size must be one of {PAGE_SIZES}, got {page}")
+    st = cache.stride()
+    if st[2] != 1 or st[1] != CACHE_DIM or (n > 1 and st[0] < page * CACHE_DIM):
+        raise ValueError("cache rows must be dense, pages must not overlap")
+    return n, page, st[0] if n > 1 else page * CACHE_DIM
+
+
+def page_plan(context_len, new_len, free_pages, block_table, page_size, num_pages, max_tokens,
+              node_depth=None, out=None, stream=None):
+    """Block tables and slot maps of one step via ``mla_page_plan``: returns
+    (cu_new [B+1], slot_map [max_tokens], positions [max_tokens], counts [2]),
+    all int32 (``out`` gives them), and writes the new pages' entries into
+    ``block_table`` [B, max_pages]."""
+    lib = load()
+    dev = _cuda_device(context_len, "context_len")
+    i32 = torch.int32
+    B = context_len.shape[0]
+    _on(dev, context_len, i32, (B,), "context_len")
+    _on(dev, new_len, i32, (B,), "new_len")
+    n_free = 0 if free_pages is None else free_pages.numel()
+    if n_free:
+        _on(dev, free_pages, i32, (n_free,), "free_pages")
+    cols = block_table.shape[1]
+    _on(dev, block_table, i32, (B, cols), "block_table")
+    if node_depth is not None:
+        _on(dev, node_depth, i32, (max_tokens,), "node_depth")
+    with _launching(dev, stream) as handle:
+        if out is None:
+            out = tuple(torch.empty(n, dtype=i32, device=dev)
+                        for n in (B + 1, max_tokens, max_tokens, 2))
+        cu, slots, pos, counts = out
+        _on(dev, cu, i32, (B + 1,), "cu_new")
+        _on(dev, slots, i32, (max_tokens,), "slot_map")
+        _on(dev, pos, i32, (max_tokens,), "positions")
+        _on(dev, counts, i32, (2,), "counts")
+        st = lib.mla_page_plan(context_len.data_ptr(), new_len.data_ptr(), B,
+                               free_pages.data_ptr() if n_free else None, n_free,
+                               _ptr(node_depth), num_pages, page_size, block_table.data_ptr(),
+                               cols, cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), max_tokens,
+                               counts.data_ptr(), handle)
+    _check("mla_page_plan", st)
+    return out
+
+
+def cache_append(c_kv, k_pe, slot_map, cache, positions=None, rope=None, stream=None):
+    """Write ``c_kv`` [N, 512] and ``k_pe`` [N, 64] into the slots of ``cache``
+    [pages, page_size, 576] via ``mla_cache_append``; ``rope`` (a mapping of
+    config.json's rotary fields) rotates k_pe at ``positions`` [N], None stores
+    it as it is. Returns ``cache``."""
+    lib = load()
+    dev = _cuda_device(c_kv, "c_kv")
+    N = c_kv.shape[0]
+    _on(dev, c_kv, torch.bfloat16, (N, KV_RANK), "c_kv")
+    _on(dev, k_pe, torch.bfloat16, (N, DR), "k_pe")
+    _on(dev, slot_map, torch.int32, (N,), "slot_map")
+    n_pages, page, stride = _cache_pages(cache, dev)
+    yr = _step_rope(rope, positions, N, dev)
+    with _launching(dev, stream) as handle:
+        st = lib.mla_cache_append(c_kv.data_ptr(), k_pe.data_ptr(),
+                                  positions.data_ptr() if yr is not None else None, yr,
+                                  slot_map.data_ptr(), N, cache.data_ptr(), n_pages, page, stride,
+                                  handle)
+    _check("mla_cache_append", st)
+    return cache
+
+
+def _step_rope(rope, positions, N, dev):
+    if rope is None:
+        return None
+    if positions is None:
+        raise ValueError("rope needs positions")
+    _on(dev, positions, torch.int32, (N,), "positions")
+    return ctypes.byref(_yarn(rope))
+
+
+def attn_tree_workspace_bytes(B: int, N: int) -> int:
+    return int(load().mla_attn_tree_workspace_bytes(B, N))
+
+
+def attn_tree(q_nope, q_pe, W_kv_b, cache, block_table, context_len, cu_new, tree_mask=None,
+              positions=None, rope=None, softmax_scale=None, out=None, workspace=None,
+              stream=None):
+    """Attention of a step's tokens (single tokens, chains or drafted trees)
+    over the paged cache, merged heads [N, 8192] bf16, via ``mla_attn_tree``.
+    ``tree_mask`` [N, words] int32 holds the visible nodes' bits (None: a
+    chain); ``rope`` rotates q_pe at ``positions`` (None: rotated already)."""
+    lib = load()
+    dev = _cuda_device(q_nope, "q_nope")
+    bf16, i32 = torch.bfloat16, torch.int32
+    N, B = q_nope.shape[0], context_len.shape[0]
+    _on(dev, q_nope, bf16, (N, H, DN), "q_nope")
+    _on(dev, q_pe, bf16, (N, H, DR), "q_pe")
+    _on(dev, W_kv_b, bf16, (H * (DN + DV), KV_RANK), "W_kv_b")
+    n_pages, page, stride = _cache_pages(cache, dev)
+    cols = block_table.shape[1]
+    _on(dev, block_table, i32, (B, cols), "block_table")
+    _on(dev, context_len, i32, (B,), "context_len")
+    _on(dev, cu_new, i32, (B + 1,), "cu_new")
+    words = 0
+    if tree_mask is not None:
+        words = tree_mask.shape[1]
+        _on(dev, tree_mask, i32, (N, words), "tree_mask")
+    yr = _step_rope(rope, positions, N, dev)
+    scale = _inputs.DEFAULT_SCALE if softmax_scale is None else float(softmax_scale)
+    with _launching(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((N, K_OPROJ), dtype=bf16, device=dev)
+        if workspace is None:
+            workspace = torch.empty(attn_tree_workspace_bytes(B, N), dtype=torch.uint8, device=dev)
+        _on(dev, out, bf16, (N, K_OPROJ), "out")
+        st = lib.mla_attn_tree(q_nope.data_ptr(), q_pe.data_ptr(), W_kv_b.data_ptr(),
+                               positions.data_ptr() if yr is not None else None, yr,
+                               cache.data_ptr(), n_pages, page, stride, block_table.data_ptr(),
+                               cols, context_len.data_ptr(), cu_new.data_ptr(), _ptr(tree_mask),
+                               words, B, N, scale, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), out.data_ptr(),
+                               handle)
+    _check("mla_attn_tree", st)
+    return out
+
+
+def quantize_weight_w4(W_o, group=128, q=None, scale=None, stream=None):
+    """4-bit codes [7168, 4096] (uint8, two a byte) and group scales
+    [7168, 8192 / group] (bf16) of ``W_o`` via ``mla_quantize_weight_w4``."""
+    lib = load()
+    dev = _cuda_device(W_o, "W_o")
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
+    _on(dev, W_o, torch.bfloat16, (D_MODEL, K_OPROJ), "W_o")
+    with _launching(dev, stream) as handle:
+        if q is None:
+            q = torch.empty((D_MODEL, K_OPROJ // 2), dtype=torch.uint8, device=dev)
+        if scale is None:
+            scale = torch.empty((D_MODEL, K_OPROJ // group), dtype=torch.bfloat16, device=dev)
+        _on(dev, q, torch.uint8, (D_MODEL, K_OPROJ // 2), "q")
+        _on(dev, scale, torch.bfloat16, (D_MODEL, K_OPROJ // group), "scale")
+        st = lib.mla_quantize_weight_w4(W_o.data_ptr(), group, q.data_ptr(), scale.data_ptr(),
+                                        handle)
+    _check("mla_quantize_weight_w4", st)
+    return q, scale
+
+
+def o_proj_w4(attn, W_q, W_scale, out=None, stream=None):
+    """o_proj with 4-bit weights -> [M, 7168] bf16 via ``mla_o_proj_w4``; the
+    group size is 8192 / W_scale's columns."""
+    lib = load()
+    dev = _cuda_device(attn, "attn")
+    M = attn.shape[0]
+    _on(dev, attn, torch.bfloat16, (M, K_OPROJ), "attn")
+    _on(dev, W_q, torch.uint8, (D_MODEL, K_OPROJ // 2), "W_q")
+    groups = W_scale.shape[1]
+    if groups not in (64, 128, 256):
+        raise ValueError(f"W_scale must have 64, 128 or 256 columns, got {groups}")
+    _on(dev, W_scale, torch.bfloat16, (D_MODEL, groups), "W_scale")
+    with _launching(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((M, D_MODEL), dtype=torch.bfloat16, device=dev)
+        _on(dev, out, torch.bfloat16, (M, D_MODEL), "out")
+        st = lib.mla_o_proj_w4(attn.data_ptr(), W_q.data_ptr(), W_scale.data_ptr(),
+                               K_OPROJ // groups, M, out.data_ptr(), handle)
+    _check("mla_o_proj_w4", st)
     return out
 
 

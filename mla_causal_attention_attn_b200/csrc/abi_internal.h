@@ -9,6 +9,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/mla.h"
+#include "rope.h"
 
 namespace mla {
 namespace abi {
@@ -59,6 +60,10 @@ mla_status_t check_attn_args(const void* q_nope, const void* q_pe, const void* k
                              int B, int T, float softmax_scale, const void* out);
 
 mla_status_t from_cuda(cudaError_t e);
+
+// The rotary parameters' frequencies; MLA_ERR_INVALID_ARG for NULL or
+// parameters out of range.
+mla_status_t rope_freqs(const mla_yarn_rope_t* rope, RopeFreqs* f);
 
 // Mask-tile classification (when mask is given, into `cls`) followed by the
 // attention kernel writing the merged heads to `out`; timeouts go to
