@@ -205,9 +205,12 @@ class Case:
                 [self.mask, np.zeros((spare, self.mask.shape[1]), np.uint32)]).view(np.int32))).to(dev)
 
     def call(self, **kw):
+        # (the lengths stay referenced: a call on another stream may still read them)
+        self.lengths = getattr(self, "lengths", None) or (i32(self.ctx, self.dev),
+                                                          i32(self.cu, self.dev))
         return binding.attn_tree(self.q_nope, self.q_pe, self.W, self.cache, self.table,
-                                 i32(self.ctx, self.dev), i32(self.cu, self.dev),
-                                 tree_mask=self.mask_t, positions=self.pos, rope=self.rope, **kw)
+                                 *self.lengths, tree_mask=self.mask_t, positions=self.pos,
+                                 rope=self.rope, **kw)
 
     def want(self):
         return ref.attn(self.q_nope, self.q_pe, self.W, self.cache, self.table, self.ctx, self.cu,
