@@ -16,6 +16,8 @@
 
 #include <cuda_bf16.h>
 
+#include <limits>
+
 #include "host_util.h"
 #include "sm100.cuh"
 
@@ -54,6 +56,7 @@ static_assert(sizeof(TreeReq) == 48, "TreeReq");
 struct Scratch {
   long long* n_items;
   TreeReq* req;        // [B]
+  int* row_req;        // [N]: the last request that starts at or before the row
   __nv_bfloat16* q;    // [N, 64, 576]
   float* o;            // [N, 64, 512], requests in one range
   float* part_o;       // [kMaxSlots][128][512]
@@ -69,6 +72,8 @@ Scratch carve(void* base, int B, int64_t N) {
   p += 256;
   s.req = reinterpret_cast<TreeReq*>(p);
   p += up256(size_t(B) * sizeof(TreeReq));
+  s.row_req = reinterpret_cast<int*>(p);
+  p += up256(size_t(N) * 4);
   s.q = reinterpret_cast<__nv_bfloat16*>(p);
   p += up256(size_t(N) * kHeads * kRow * 2);
   s.o = reinterpret_cast<float*>(p);
@@ -198,79 +203,123 @@ __device__ __forceinline__ void cp_wait() {
 }
 
 // ---------------------------------------------------------------- query
-// q~ = U_h^T q_nope: 16 tokens x 128 latent columns per CTA, contraction over
-// the head's 128 key dims. Grid: (64 heads * 4 column quarters, token tiles);
-// the CTA (0, y = token tiles) lays out the schedule instead.
+// q~ = U_h^T q_nope: 16 tokens x 128 latent columns a step, contraction over
+// the head's 128 key dims. Grid (64 heads * 4 column quarters, y + 1): a CTA
+// keeps its 32 KB of weights in shared memory and walks every y-th token tile,
+// the next one on its way. The CTAs of the last y row do the rest: the first
+// lays out the schedule and clears the status word, the others rotate the
+// rotary parts (a warp turns 8 heads of a token by one sine and cosine per
+// lane) and find the rows' requests.
 constexpr int kQTok = 16;
 constexpr int kQThreads = 256;
 constexpr int kQCols = 128;
 constexpr int kQLd = 128 + 8;  // padded rows, in elements
+constexpr int kQHeads = 8;     // heads a warp rotates with one angle
+
+template <bool kRope>
+__device__ void rotate_queries(const AttnTreeArgs& a, const Scratch& s, const RopeFreqs& f, int part,
+                               int parts) {
+  const int lane = threadIdx.x & 31;
+  const int warps = kQThreads / 32;
+  const double freq = kRope ? f.inv_freq[lane] : 0.0;
+  const auto* qp = static_cast<const __nv_bfloat162*>(a.q_pe);
+  for (int64_t i = int64_t(part) * warps + (threadIdx.x >> 5); i < int64_t(a.N) * (kHeads / kQHeads);
+       i += int64_t(parts) * warps) {
+    const int64_t n = i / (kHeads / kQHeads);
+    const int64_t row = n * kHeads + i % (kHeads / kQHeads) * kQHeads;
+    __nv_bfloat162 y[kQHeads];
+#pragma unroll
+    for (int k = 0; k < kQHeads; ++k) y[k] = qp[(row + k) * kRopePairs + lane];
+    if (kRope) {
+      double sn, cs;
+      sincos(double(a.positions[n]) * freq, &sn, &cs);
+      cs *= f.attn_factor;
+      sn *= f.attn_factor;
+#pragma unroll
+      for (int k = 0; k < kQHeads; ++k) {
+        const double u = __bfloat162float(y[k].x), v = __bfloat162float(y[k].y);
+        y[k].x = __double2bfloat16(u * cs - v * sn);
+        y[k].y = __double2bfloat16(v * cs + u * sn);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kQHeads; ++k)
+      reinterpret_cast<__nv_bfloat162*>(s.q + (row + k) * kRow + kLat)[lane] = y[k];
+  }
+  for (int n = part * kQThreads + threadIdx.x; n < a.N; n += parts * kQThreads) {
+    int l = 0, h = a.B;
+    while (h - l > 1) {
+      const int m = (l + h) >> 1;
+      if (a.cu_new[m] <= n) l = m;
+      else h = m;
+    }
+    s.row_req[n] = l;
+  }
+}
 
 template <bool kRope>
 __global__ void __launch_bounds__(kQThreads)
-    tree_query_kernel(const AttnTreeArgs a, const Scratch s, const RopeFreqs f, int clusters) {
-  if (int(blockIdx.y) == int(gridDim.y) - 1) {
-    if (blockIdx.x == 0) schedule(a, s, clusters);
+    tree_query_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
+                      const __grid_constant__ RopeFreqs f, int clusters, unsigned int* err_word) {
+  if (blockIdx.y == gridDim.y - 1) {
+    if (blockIdx.x == 0) {
+      if (threadIdx.x == 0) *err_word = 0u;
+      schedule(a, s, clusters);
+    } else {
+      rotate_queries<kRope>(a, s, f, blockIdx.x - 1, gridDim.x - 1);
+    }
     return;
   }
-  __shared__ __align__(16) __nv_bfloat16 sq[kQTok * kQLd];
+  __shared__ __align__(16) __nv_bfloat16 sq[2][kQTok * kQLd];
   __shared__ __align__(16) __nv_bfloat16 sw[kNope * kQLd];
   const int h = blockIdx.x >> 2, c0 = (blockIdx.x & 3) * kQCols;
-  const int n0 = blockIdx.y * kQTok;
+  const int tiles = (a.N + kQTok - 1) / kQTok, step = gridDim.y - 1;
   const auto* qn = static_cast<const __nv_bfloat16*>(a.q_nope);
   const auto* w = static_cast<const __nv_bfloat16*>(a.w_kv_b) + size_t(h) * 256 * kLat + c0;
+  static_assert(kQTok * (kNope / 8) == kQThreads, "one piece of a query tile per thread");
+  auto load = [&](int tile, int buf) {
+    const int n = threadIdx.x / (kNope / 8), c = threadIdx.x % (kNope / 8) * 8;
+    const int row = min(tile * kQTok + n, a.N - 1);
+    cp16(smem_u32(&sq[buf][n * kQLd + c]), qn + (size_t(row) * kHeads + h) * kNope + c, true);
+    cp_commit();
+  };
   for (int i = threadIdx.x; i < kNope * (kQCols / 8); i += kQThreads) {
     const int e = i / (kQCols / 8), c = i % (kQCols / 8) * 8;
     cp16(smem_u32(sw + e * kQLd + c), w + size_t(e) * kLat + c, true);
   }
-  for (int i = threadIdx.x; i < kQTok * (kNope / 8); i += kQThreads) {
-    const int n = i / (kNope / 8), c = i % (kNope / 8) * 8;
-    const int row = min(n0 + n, a.N - 1);
-    cp16(smem_u32(sq + n * kQLd + c), qn + (size_t(row) * kHeads + h) * kNope + c, true);
-  }
-  cp_commit();
-  if (c0 == 0) {
-    // the rotary part of these tokens' queries: one pair per thread
-    const auto* qp = static_cast<const __nv_bfloat162*>(a.q_pe);
-    for (int i = threadIdx.x; i < kQTok * kRopePairs; i += kQThreads) {
-      const int n = n0 + i / kRopePairs, p = i % kRopePairs;
-      if (n >= a.N) continue;
-      __nv_bfloat162 y = qp[(size_t(n) * kHeads + h) * kRopePairs + p];
-      if (kRope) {
-        double sn, cs;
-        sincos(double(a.positions[n]) * f.inv_freq[p], &sn, &cs);
-        cs *= f.attn_factor;
-        sn *= f.attn_factor;
-        const double u = __bfloat162float(y.x), v = __bfloat162float(y.y);
-        y.x = __double2bfloat16(u * cs - v * sn);
-        y.y = __double2bfloat16(v * cs + u * sn);
-      }
-      reinterpret_cast<__nv_bfloat162*>(s.q + (size_t(n) * kHeads + h) * kRow + kLat)[p] = y;
-    }
-  }
-  cp_wait<0>();
-  __syncthreads();
+  load(blockIdx.y, 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cw = warp * 16;  // this warp's 16 columns: two n-tiles
-  float d[2][4] = {};
-#pragma unroll
-  for (int k = 0; k < kNope / 16; ++k) {
-    uint32_t fa[4], fb[4];
-    ldsm4(fa, smem_u32(sq + (lane & 15) * kQLd + k * 16 + (lane >> 4) * 8));
-    ldsm4t(fb, smem_u32(sw + (k * 16 + (lane & 15)) * kQLd + cw + (lane >> 4) * 8));
-    mma_16816(d[0], fa, fb[0], fb[1]);
-    mma_16816(d[1], fa, fb[2], fb[3]);
-  }
   const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int n = n0 + g + 8 * half;
-      if (n < a.N)
-        *reinterpret_cast<uint32_t*>(s.q + (size_t(n) * kHeads + h) * kRow + c0 + cw + 8 * j + 2 * t) =
-            pack_bf16x2(d[j][2 * half], d[j][2 * half + 1]);
+  int buf = 0;
+  for (int tile = blockIdx.y; tile < tiles; tile += step, buf ^= 1) {
+    if (tile + step < tiles) {
+      load(tile + step, buf ^ 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
     }
+    __syncthreads();
+    float d[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < kNope / 16; ++k) {
+      uint32_t fa[4], fb[4];
+      ldsm4(fa, smem_u32(&sq[buf][(lane & 15) * kQLd + k * 16 + (lane >> 4) * 8]));
+      ldsm4t(fb, smem_u32(sw + (k * 16 + (lane & 15)) * kQLd + cw + (lane >> 4) * 8));
+      mma_16816(d[0], fa, fb[0], fb[1]);
+      mma_16816(d[1], fa, fb[2], fb[3]);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int n = tile * kQTok + g + 8 * half;
+        if (n < a.N)
+          *reinterpret_cast<uint32_t*>(s.q + (size_t(n) * kHeads + h) * kRow + c0 + cw + 8 * j +
+                                       2 * t) = pack_bf16x2(d[j][2 * half], d[j][2 * half + 1]);
+      }
+    __syncthreads();  // the buffer is loaded again two tiles later
+  }
 }
 
 // ---------------------------------------------------------------- attention
@@ -295,8 +344,9 @@ __device__ __forceinline__ Item find_item(const AttnTreeArgs& a, const Scratch& 
   const int k = int(i - it.r.item);
   it.range = k / pairs;
   it.pair = k % pairs;
-  it.t0 = int((long long)it.r.tiles * it.range / it.r.ranges);
-  it.t1 = int((long long)it.r.tiles * (it.range + 1) / it.r.ranges);
+  // (ranges <= clusters, so the products stay below 2^31)
+  it.t0 = int(unsigned(it.r.tiles) * unsigned(it.range) / unsigned(it.r.ranges));
+  it.t1 = int(unsigned(it.r.tiles) * unsigned(it.range + 1) / unsigned(it.r.ranges));
   return it;
 }
 
@@ -322,11 +372,9 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // The cache goes through shared memory once as K (128 keys x 64 dims a block)
 // and, two tiles later and from L2, as V (64 keys x 128 latent columns a
 // block): the halves of the pair that the two products need differ. Blocks of
-// both kinds are 16 KB and share one ring of seven; the issuer alternates the
-// score product of tile j + 2 with the value product of tile j, block by
-// block, while the softmax of tile j + 1 runs:
-//   K_0 K_1 | K_2,0 V_0,0 K_2,1 V_0,1 .. V_0,7 K_2,8 | K_3,0 V_1,0 ..
-// so that both are consumed evenly and a block has 6 * 258 clocks to arrive.
+// both kinds are 16 KB, in a ring of four (K) and one of three (V). The score
+// products of tile j + 2 and the value products of tile j, issued by a thread
+// each, share the tensor core while the softmax of tile j + 1 runs.
 // Key 128 r + c of a tile is column c of lanes 64 r ..: softmax thread t of 128
 // has row t % 64 and 128 of the keys; both threads of a row keep one running
 // maximum.
@@ -338,19 +386,25 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // 64-key chunk (0 * NaN is NaN): those two blocks complete on a barrier of
 // their own CTA, a warp zeroes the rows and then reports the bytes to the ring.
 //
+// Instructions are the scarce resource: eight roles share one instruction
+// cache, and with unrolled blocks and waits inline (250 KB of code) the kernel
+// ran at a tenth of its speed from cache misses. So loops over blocks stay
+// rolled, waits that do not succeed at once are out of line, and masks are
+// applied by a rolled pass over the few tiles that need one.
+//
 // Every wait is bounded; the teardown is the pair kernel's of attn_prefill.cu.
-constexpr int kAThreads = 256;
+constexpr int kAThreads = 320;
 constexpr uint32_t kBlk = 16384;                 // ring block
-constexpr int kRing = 7;
+constexpr int kKRing = 4, kVRing = 3;
 constexpr int kKBlocks = kRow / 64;              // 9 K blocks a tile
 constexpr int kVBlocks = 8;                      // 4 chunks of 64 keys x 2 products
 constexpr uint32_t kQBlk = 64 * 128;             // one 64-dim block of a node's query rows
 constexpr uint32_t kOffP = kKBlocks * kQBlk;     // P: 4 chunks of [64 rows][64 keys]
 constexpr uint32_t kOffRing = kOffP + 4 * kQBlk;
-constexpr size_t kASmem = kOffRing + kRing * kBlk + 1024;
+constexpr uint32_t kOffV = kOffRing + kKRing * kBlk;
+constexpr size_t kASmem = kOffV + kVRing * kBlk + 1024;
 static_assert(kASmem <= 225 * 1024, "shared memory budget");
 constexpr uint32_t kColO = 0, kColS = 256;       // tensor memory columns
-constexpr uint16_t kBoth = 0x3;
 constexpr float kRescale = 8.f;                  // log2 growth of the maximum that rescales O
 
 // What a cluster visits: its items one after another, tile by tile.
@@ -360,7 +414,9 @@ struct Walk {
   long long next_item, n_items, step;
   Item it;
   int b, tile;
-  int item_no;  // items begun so far - 1
+  int item_no;   // items begun so far - 1
+  int cut_last;  // cut chunk of the item's last tile, or -1
+  int cut_row;   // its first row without a key
 
   __device__ __forceinline__ Walk(const AttnTreeArgs& aa, const Scratch& ss, long long first,
                                   long long n, long long st)
@@ -376,18 +432,62 @@ struct Walk {
     tile = it.t0;
     next_item += step;
     ++item_no;
+    // The chunk of 64 keys that the request's last key lies in has rows to be
+    // zeroed when a TMA box (min(page, 64) rows) goes past that key.
+    const int box = a->page_shift >= 6 ? 64 : 1 << a->page_shift;
+    cut_last = -1;
+    if (it.t1 == it.r.tiles && (it.r.keys & (box - 1)) != 0) {
+      cut_last = ((it.r.keys - 1) & (kTileKeys - 1)) >> 6;
+      cut_row = it.r.keys & 63;
+    }
     return true;
   }
   __device__ __forceinline__ bool first() const { return tile == it.t0; }
   __device__ __forceinline__ bool last() const { return tile + 1 == it.t1; }
-  // Rows of the tile's chunk c that hold keys, when a block of R rows is cut
-  // inside the chunk; -1 when no row needs to be zeroed.
-  __device__ __forceinline__ int cut(int c, int R) const {
-    if (tile + 1 != it.r.tiles || it.r.keys % R == 0) return -1;
-    const int e = it.r.keys - tile * kTileKeys;
-    return e / 64 == c ? e % 64 : -1;
+  // The tile's chunk with rows to be zeroed, or -1.
+  __device__ __forceinline__ int cut() const { return last() ? cut_last : -1; }
+};
+
+// A position in a ring: slot and parity of its pass.
+template <int kSlots>
+struct RingPos {
+  uint32_t slot = 0, par = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == uint32_t(kSlots)) {
+      slot = 0;
+      par ^= 1u;
+    }
   }
 };
+
+// The kernel's waits; a wait that does not succeed at once loops out of line.
+struct Waits {
+  int* abort_flag;
+  unsigned int* err_word;
+  unsigned long long limit_ns;
+};
+
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, const Waits w,
+                                       uint32_t site) {
+  const WaitCtl ctl{w.abort_flag, w.limit_ns, kErrKernelTree, w.err_word};
+  return mbar_wait_cluster_sleep(bar, parity, ctl, site);
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Waits& w,
+                                         uint32_t site) {
+  return mbar_try_wait(bar, parity) || wait_more(bar, parity, w, site);
+}
+
+// Warp-uniform result.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Waits& w,
+                                          uint32_t site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_more(bar, parity, w, site));
+}
+
+__device__ __forceinline__ void fence_acq_rel_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
 
 __device__ __forceinline__ uint32_t mask_window(const uint32_t* mask, int words, int d) {
   // bits d .. d + 31 of the mask row (bits outside it are 0)
@@ -420,11 +520,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmC,
                      const __grid_constant__ AttnTreeArgs a,
-                     const __grid_constant__ Scratch s, float scale_log2, int box_rows,
+                     const __grid_constant__ Scratch s, float scale_log2,
                      unsigned long long wait_limit_ns, unsigned int* err_word, int test_stall) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[kRing];    // even CTA: both CTAs' halves of a block landed
-  __shared__ uint64_t empty[kRing];   // this CTA's block is free
+  __shared__ uint64_t k_full[kKRing];   // even CTA: both CTAs' halves of a block landed
+  __shared__ uint64_t k_empty[kKRing];  // this CTA's block is free
+  __shared__ uint64_t v_full[kVRing];
+  __shared__ uint64_t v_empty[kVRing];
   __shared__ uint64_t q_full[kKBlocks];   // even CTA: both CTAs' query blocks landed
   __shared__ uint64_t q_empty[kKBlocks];  // the item's last score product has read the block
   __shared__ uint64_t s_full[2];      // scores are in buffer b
@@ -434,27 +536,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   __shared__ uint64_t p_free[2];      // the value products have read P of key half h
   __shared__ uint64_t o_free;         // O of an item is read (even / odd as s_free)
   __shared__ uint64_t cut_full[2];    // this CTA's cut V block of product m landed
-  __shared__ uint64_t drain_bar;
+  __shared__ uint64_t drain_bar[2];   // the two issuers' products in flight
   __shared__ uint64_t never_bar;      // no thread ever arrives (failure-detection test)
-  __shared__ uint32_t n_issued[2];    // ring blocks, query blocks this CTA's producer issued
+  __shared__ uint32_t n_issued[3];    // K, V and query blocks this CTA's producers issued
   __shared__ uint32_t n_cut[2];       // cut blocks issued, reported
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ float xch[2][64];        // a row's two halves: maximum or sum
+  __shared__ float xch[2][2][64];     // maxima of a row's two halves, by parity of the tile
+  __shared__ float xsum[2][64];       // sums of a row's two halves
 
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  WaitCtl ctl{&abort_flag, wait_limit_ns, kErrKernelTree, err_word};
+  const Waits waits{&abort_flag, err_word, wait_limit_ns};
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    n_issued[0] = n_issued[1] = n_cut[0] = n_cut[1] = 0;
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    n_issued[0] = n_issued[1] = n_issued[2] = n_cut[0] = n_cut[1] = 0;
+    for (int i = 0; i < kKRing; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < kVRing; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < kKBlocks; ++i) {
       mbar_init(&q_full[i], 1);
@@ -466,9 +573,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       mbar_init(&p_full[i], (i == 0 ? 4 : 2) + (leader ? 1 : 0));
       mbar_init(&p_free[i], 1);
       mbar_init(&cut_full[i], 1);
+      mbar_init(&drain_bar[i], 1);
     }
     mbar_init(&o_free, leader ? 5 : 4);
-    mbar_init(&drain_bar, 1);
     mbar_init(&never_bar, 1);
     fence_barrier_init();
   }
@@ -485,233 +592,221 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   const long long first_item = blockIdx.x >> 1, step = gridDim.x >> 1;
   Walk walk(a, s, first_item, n_items, step);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    // All lanes: one TMA copy each (a block is 2 to 8 pieces of pages).
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ producers
+    // warp 0: query and K blocks, warp 2: V blocks. All lanes: one TMA copy
+    // each (a block is 2 to 8 pieces of pages); lane i knows the page of box i
+    // of the tile.
     if (lane == 0) {
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmC);
     }
-    const int R = box_rows;
-    uint32_t seq = 0, qseq = 0;
-    bool ok = true;
-    // arms (even CTA) the block's barrier and returns its address in the even CTA
-    auto claim = [&]() -> uint32_t {
-      const uint32_t slot = seq % kRing, par = (seq / kRing) & 1u;
-      ok = mbar_wait_warp(&empty[slot], par ^ 1u, ctl, 1);
-      if (ok && lane == 0) {
-        if (leader) mbar_arrive_expect_tx(&full[slot], 2 * kBlk);
-        n_issued[0] = seq + 1;
-      }
-      __syncwarp();
-      return mapa_shared(smem_u32(&full[slot]), 0);
-    };
-    auto key_page = [&](const Walk& w, int key) -> int {  // page, or one past the last: zeros
-      const int id = key < w.it.r.keys ? page_of(a, w.b, key) : -1;
+    const int box_shift = a.page_shift >= 6 ? 6 : a.page_shift;
+    const int per = 64 >> box_shift;  // boxes a 64-key chunk
+    const int pmask = (1 << a.page_shift) - 1;
+    auto page_at = [&](int key) -> int {  // page, or one past the last: zeros
+      const int id = key < walk.it.r.keys ? page_of(a, walk.b, key) : -1;
       return id >= 0 ? id : a.num_pages;
     };
-    const int pmask = (1 << a.page_shift) - 1;
-    auto load_q = [&](const Walk& w, int blk) {
-      ok = mbar_wait_warp(&q_empty[blk], uint32_t(w.item_no & 1) ^ 1u, ctl, 2);
-      if (!ok) return;
-      if (lane == 0) {
-        if (leader) mbar_arrive_expect_tx(&q_full[blk], 2 * kQBlk);
-        n_issued[1] = ++qseq;
-        const int node = 2 * w.it.pair + int(rank);
-        const int row = node < w.it.r.nodes ? (w.it.r.start + node) * kHeads : a.N * kHeads;
-        tma_load_2d_pair(smem + blk * kQBlk, &tmQ, mapa_shared(smem_u32(&q_full[blk]), 0),
-                         blk * 64, row);
-      }
-      __syncwarp();
-    };
-    auto load_k = [&](const Walk& w, int blk, int key, int page) {
-      if (w.first()) load_q(w, blk);
-      if (!ok) return;
-      const uint32_t bar = claim();
-      if (!ok) return;
-      uint8_t* dst = smem + kOffRing + (seq % kRing) * kBlk;
-      if (lane < 128 / R)
-        tma_load_3d_pair(dst + lane * R * 128, &tmC, bar, blk * 64, key & pmask, page);
-      ++seq;
-    };
-    auto load_v = [&](const Walk& w, int blk) {
-      const uint32_t bar = claim();
-      if (!ok) return;
-      uint8_t* dst = smem + kOffRing + (seq % kRing) * kBlk;
-      const int c = blk >> 1, m = blk & 1;
-      const int per = 64 / R;
-      uint32_t to = bar;
-      if (w.cut(c, R) >= 0) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&cut_full[m], kBlk);
-          n_cut[0] = n_cut[0] + 1;
+    uint32_t issued = 0;
+    bool ok = true;
+    if (warp == 0) {
+      RingPos<kKRing> pos;
+      uint32_t q_issued = 0;
+      const uint32_t full0 = mapa_shared(smem_u32(&k_full[0]), 0);
+      const uint32_t q_full0 = mapa_shared(smem_u32(&q_full[0]), 0);
+      while (ok && walk.next()) {
+        const int key = walk.tile * kTileKeys + int(rank) * 128 + (lane << box_shift);
+        const int page = lane < 2 * per ? page_at(key) : 0;
+        const bool first = walk.first();
+        const int node = 2 * walk.it.pair + int(rank);
+        const int qrow =
+            node < walk.it.r.nodes ? (walk.it.r.start + node) * kHeads : a.N * kHeads;  // zeros
+#pragma unroll 1
+        for (int i = 0; ok && i < kKBlocks; ++i) {
+          if (first) {
+            ok = wait_warp(&q_empty[i], uint32_t(walk.item_no & 1) ^ 1u, waits, 2);
+            if (!ok) break;
+            ++q_issued;
+            if (lane == 0) {
+              if (leader) mbar_arrive_expect_tx(&q_full[i], 2 * kQBlk);
+              n_issued[2] = q_issued;
+              tma_load_2d_pair(smem + i * kQBlk, &tmQ, q_full0 + i * 8, i * 64, qrow);
+            }
+          }
+          ok = wait_warp(&k_empty[pos.slot], pos.par ^ 1u, waits, 1);
+          if (!ok) break;
+          ++issued;
+          // (bytes that land before the barrier is armed are counted all the same)
+          if (lane == 0) {
+            if (leader) mbar_arrive_expect_tx(&k_full[pos.slot], 2 * kBlk);
+            n_issued[0] = issued;
+          }
+          if (lane < 2 * per)
+            tma_load_3d_pair(smem + kOffRing + pos.slot * kBlk + (lane << box_shift) * 128, &tmC,
+                             full0 + pos.slot * 8, i * 64, key & pmask, page);
+          pos.advance();
         }
-        __syncwarp();
-        to = mapa_shared(smem_u32(&cut_full[m]), rank);
       }
-      if (lane < 2 * per) {
-        const int j = lane / per, i = lane % per;
-        const int key = w.tile * kTileKeys + c * 64 + i * R;
-        tma_load_3d_pair(dst + j * 8192 + i * R * 128, &tmC, to,
-                         m * 256 + int(rank) * 128 + j * 64, key & pmask, key_page(w, key));
+    } else {
+      RingPos<kVRing> pos;
+      const uint32_t full0 = mapa_shared(smem_u32(&v_full[0]), 0);
+      const uint32_t cut0 = mapa_shared(smem_u32(&cut_full[0]), rank);
+      const int vi = lane & (per - 1), vj = lane >> (6 - box_shift);  // box, 64-column half
+      uint32_t cuts = 0;
+      while (ok && walk.next()) {
+        const int tile_key = walk.tile * kTileKeys;
+        const int pages = lane < 4 * per ? page_at(tile_key + (lane << box_shift)) : 0;
+        const int cut = walk.cut();
+#pragma unroll 1
+        for (int i = 0; i < kVBlocks; ++i) {
+          const int c = i >> 1, m = i & 1;
+          const int page = __shfl_sync(0xffffffffu, pages, c * per + vi);
+          ok = wait_warp(&v_empty[pos.slot], pos.par ^ 1u, waits, 3);
+          if (!ok) break;
+          ++issued;
+          if (lane == 0) {
+            if (leader) mbar_arrive_expect_tx(&v_full[pos.slot], 2 * kBlk);
+            n_issued[1] = issued;
+          }
+          uint32_t bar = full0 + pos.slot * 8;
+          if (c == cut) {
+            ++cuts;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&cut_full[m], kBlk);
+              n_cut[0] = cuts;
+            }
+            bar = cut0 + m * 8;
+          }
+          if (lane < 2 * per)
+            tma_load_3d_pair(smem + kOffV + pos.slot * kBlk + vj * 8192 + (vi << box_shift) * 128,
+                             &tmC, bar, m * 256 + int(rank) * 128 + vj * 64,
+                             (tile_key + c * 64 + (vi << box_shift)) & pmask, page);
+          pos.advance();
+        }
       }
-      ++seq;
-    };
-    Walk wv = walk;
-    auto k_page = [&](int& key) -> int {
-      key = walk.tile * kTileKeys + int(rank) * 128 + lane * R;
-      return lane < 128 / R ? key_page(walk, key) : 0;
-    };
-    bool more = walk.next();
-    for (int g = 0; ok && more && g < 2; ++g) {
-      int key;
-      const int page = k_page(key);
-      for (int i = 0; ok && i < kKBlocks; ++i) load_k(walk, i, key, page);
-      more = walk.next();
-    }
-    while (ok && wv.next()) {
-      int key = 0, page = 0;
-      if (more) page = k_page(key);
-      for (int i = 0; ok && i < kKBlocks; ++i) {
-        if (more) load_k(walk, i, key, page);
-        if (ok && i < kVBlocks) load_v(wv, i);
-      }
-      if (more) more = walk.next();
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (even CTA)
+    // ------------------------------------------------------------ score products (even CTA)
     if (lane == 0 && leader) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 256, false, false);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(128, 256, false, true);
-      const uint32_t base = smem_u32(smem);
-      uint32_t seq = 0;
-      bool ok = true, issued_any = false;
-      auto wait_block = [&](bool cut) -> uint32_t {
-        uint64_t* bar = &full[seq % kRing];
-        const uint32_t par = (seq / kRing) & 1u;
-        // (a cut block is reported by a thread of either CTA)
-        ok = cut ? mbar_wait_cluster_sleep(bar, par, ctl, 4) : mbar_wait(bar, par, ctl, 4);
-        tc_fence_after();
-        return base + kOffRing + (seq % kRing) * kBlk;
-      };
-      auto issue_k = [&](const Walk& w, int g, int blk) {
-        if (w.first()) ok = mbar_wait(&q_full[blk], uint32_t(w.item_no & 1), ctl, 5);
-        if (!ok) return;
-        const uint32_t kb = wait_block(false);
-        if (!ok) return;
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 256, false, false);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem) + kOffRing, 16, 1024);
+      RingPos<kKRing> pos;
+      bool ok = true, any = false;
+      for (int g = 0; ok && walk.next(); ++g) {
+        const bool first = walk.first(), last = walk.last();
         const uint32_t d = tmem + kColS + 128u * uint32_t(g & 1);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss_pair(d, sdesc_sw128(base + blk * kQBlk + kk * 32, 16, 1024),
-                      sdesc_sw128(kb + kk * 32, 16, 1024), idesc_s, (blk | kk) != 0 ? 1u : 0u);
-        issued_any = true;
-        mma_commit_pair_mc(&empty[seq % kRing], kBoth);
-        ++seq;
-        if (w.last()) mma_commit_pair_mc(&q_empty[blk], kBoth);
-        if (blk == kKBlocks - 1) mma_commit_pair_mc(&s_full[g & 1], kBoth);
-      };
-      auto issue_v = [&](const Walk& w, int blk) {
-        const int c = blk >> 1, m = blk & 1;
-        const uint32_t vb = wait_block(w.cut(c, box_rows) >= 0);
-        if (!ok) return;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss_pair(tmem + kColO + m * 128,
-                      sdesc_sw128(base + kOffP + c * kQBlk + kk * 32, 16, 1024),
-                      sdesc_sw128(vb + kk * 16 * 128, 8192, 1024), idesc_o,
-                      (!w.first() || c > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_pair_mc(&empty[seq % kRing], kBoth);
-        ++seq;
-        if (blk == 3) mma_commit_pair_mc(&p_free[0], kBoth);
-        if (blk == 7) mma_commit_pair_mc(&p_free[1], kBoth);
-      };
-      Walk wv = walk;
-      bool more = walk.next();
-      int gk = 0;
-      for (; ok && more && gk < 2; ++gk) {
-        for (int i = 0; ok && i < kKBlocks; ++i) issue_k(walk, gk, i);
-        more = walk.next();
-      }
-      for (int g = 0; ok && wv.next(); ++g) {
-        if (more) ok = mbar_wait_cluster_sleep(&s_free[g & 1], uint32_t(g >> 1) & 1u, ctl, 6);
+        if (g >= 2) ok = wait_more(&s_free[g & 1], uint32_t((g >> 1) - 1) & 1u, waits, 6);
+#pragma unroll 1
         for (int i = 0; ok && i < kKBlocks; ++i) {
-          if (more) issue_k(walk, gk, i);
-          if (!ok || i == kVBlocks) break;
-          if (i == 0) {
-            ok = mbar_wait_cluster_sleep(&p_full[0], uint32_t(g) & 1u, ctl, 7);
-            if (ok && wv.first() && wv.item_no > 0)
-              ok = mbar_wait_cluster_sleep(&o_free, uint32_t(wv.item_no - 1) & 1u, ctl, 8);
-          }
-          if (i == 4) ok = mbar_wait_cluster_sleep(&p_full[1], uint32_t(g) & 1u, ctl, 9);
-          if (ok) issue_v(wv, i);
+          if (first) ok = wait_more(&q_full[i], uint32_t(walk.item_no & 1), waits, 5);
+          ok = ok && wait_bar(&k_full[pos.slot], pos.par, waits, 4);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qd = q_desc + i * (kQBlk >> 4);
+          const uint64_t kd = k_desc + pos.slot * (kBlk >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss_pair(d, qd + kk * 2, kd + kk * 2, idesc, (i | kk) != 0 ? 1u : 0u);
+          any = true;
+          mma_commit_pair_mc(&k_empty[pos.slot], 0x3);
+          if (last) mma_commit_pair_mc(&q_empty[i], 0x3);
+          pos.advance();
         }
-        if (more) {
-          ++gk;
-          more = walk.next();
-        }
+        if (ok) mma_commit_pair_mc(&s_full[g & 1], 0x3);
       }
-      if (!ok && issued_any) {
-        mma_commit_pair_mc(&drain_bar, 0x1);
+      if (!ok && any) {
+        mma_commit_pair_mc(&drain_bar[0], 0x1);
         int zero = 0;
-        WaitCtl drain{&zero, wait_limit_ns, kErrKernelTree, err_word};
-        mbar_wait(&drain_bar, 0, drain, 10);
-      }
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ helper (odd CTA): P
-    if (lane == 0 && !leader) {
-      for (int g = 0; walk.next(); ++g) {
-        bool ok = true;
-        for (int h = 0; ok && h < 2; ++h) {
-          ok = mbar_wait(&p_full[h], uint32_t(g) & 1u, ctl, 11);
-          if (ok) mbar_arrive_cluster(mapa_shared(smem_u32(&p_full[h]), 0));
-        }
-        if (!ok) break;
+        wait_more(&drain_bar[0], 0, Waits{&zero, err_word, wait_limit_ns}, 10);
       }
     }
   } else if (warp == 3) {
-    // ------------------------------------------------------------ helper: S, O, cut blocks
-    uint32_t seq = 0;  // of the tile's first V block
-    Walk ahead = walk;
-    bool more = ahead.next();
-    for (int g = 0; more && g < 2; ++g) {
-      seq += kKBlocks;
-      more = ahead.next();
+    // ------------------------------------------------------------ value products (even CTA)
+    if (lane == 0 && leader) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 256, false, true);
+      const uint64_t p_desc = sdesc_sw128(smem_u32(smem) + kOffP, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem) + kOffV, 8192, 1024);
+      RingPos<kVRing> pos;
+      bool ok = true, any = false;
+      for (int g = 0; ok && walk.next(); ++g) {
+        const bool first = walk.first();
+        const int cut = walk.cut();
+        ok = wait_more(&p_full[0], uint32_t(g) & 1u, waits, 7);
+        if (first && walk.item_no > 0)
+          ok = ok && wait_more(&o_free, uint32_t(walk.item_no - 1) & 1u, waits, 8);
+#pragma unroll 1
+        for (int i = 0; ok && i < kVBlocks; ++i) {
+          if (i == 4) ok = wait_more(&p_full[1], uint32_t(g) & 1u, waits, 9);
+          ok = ok && wait_bar(&v_full[pos.slot], pos.par, waits, 14);
+          if (!ok) break;
+          const int c = i >> 1, m = i & 1;
+          if (c == cut) fence_acq_rel_cluster();  // (reported by a thread of either CTA)
+          tc_fence_after();
+          const uint32_t d = tmem + kColO + m * 128;
+          const uint64_t pd = p_desc + c * (kQBlk >> 4);
+          const uint64_t vd = v_desc + pos.slot * (kBlk >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss_pair(d, pd + kk * 2, vd + kk * (16 * 128 >> 4), idesc,
+                        (!first || c > 0 || kk > 0) ? 1u : 0u);
+          any = true;
+          mma_commit_pair_mc(&v_empty[pos.slot], 0x3);
+          if ((i & 3) == 3) mma_commit_pair_mc(&p_free[i >> 2], 0x3);
+          pos.advance();
+        }
+      }
+      if (!ok && any) {
+        mma_commit_pair_mc(&drain_bar[1], 0x1);
+        int zero = 0;
+        wait_more(&drain_bar[1], 0, Waits{&zero, err_word, wait_limit_ns}, 18);
+      }
     }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ helper (odd CTA): P
+    if (lane == 0 && !leader) {
+      bool ok = true;
+      for (int g = 0; ok && walk.next(); ++g)
+#pragma unroll 1
+        for (int h = 0; ok && h < 2; ++h) {
+          ok = wait_more(&p_full[h], uint32_t(g) & 1u, waits, 11);
+          if (ok) mbar_arrive_cluster(mapa_shared(smem_u32(&p_full[h]), 0));
+        }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ helper: S, O, cut blocks
     bool ok = true;
     uint32_t cuts = 0;
     for (int g = 0; ok && walk.next(); ++g) {
       if (!leader) {
-        ok = mbar_wait_warp(&s_free[g & 1], uint32_t(g >> 1) & 1u, ctl, 12);
+        ok = wait_warp(&s_free[g & 1], uint32_t(g >> 1) & 1u, waits, 12);
         if (ok && lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_free[g & 1]), 0));
       }
-      // ring position of V block i of this tile: K and V blocks alternate
-      for (int i = 0; ok && i < kVBlocks; ++i) {
-        const int v = walk.cut(i >> 1, box_rows);
-        if (v < 0) continue;
-        const uint32_t at = seq + (more ? 2 * i + 1 : i);
-        const int m = i & 1;
-        ok = mbar_wait_warp(&cut_full[m], (cuts >> 1) & 1u, ctl, 13);
-        if (!ok) break;
-        uint8_t* blk = smem + kOffRing + (at % kRing) * kBlk;
-        for (int e = lane; e < (64 - v) * 16; e += 32) {  // 2 x 8 pieces of 16 bytes a row
-          const int row = v + (e >> 4);
-          *reinterpret_cast<uint4*>(blk + ((e >> 3) & 1) * 8192 + row * 128 + (e & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
+      const int cut = walk.cut();
+      if (cut >= 0)
+#pragma unroll 1
+        for (int m = 0; ok && m < 2; ++m) {
+          const uint32_t slot = (uint32_t(g) * kVBlocks + 2 * cut + m) % kVRing;
+          ok = wait_warp(&cut_full[m], (cuts >> 1) & 1u, waits, 13);
+          if (!ok) break;
+          uint8_t* blk = smem + kOffV + slot * kBlk;
+          for (int e = lane; e < (64 - walk.cut_row) * 16; e += 32) {  // 2 x 8 pieces of 16 bytes
+            const int row = walk.cut_row + (e >> 4);
+            *reinterpret_cast<uint4*>(blk + ((e >> 3) & 1) * 8192 + row * 128 + (e & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          fence_acq_rel_cluster();
+          __syncwarp();
+          ++cuts;
+          if (lane == 0) {
+            n_cut[1] = cuts;
+            mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
+          }
         }
-        fence_proxy_async_smem();
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          n_cut[1] = ++cuts;
-          mbar_complete_tx_cluster(mapa_shared(smem_u32(&full[at % kRing]), 0), kBlk);
-        }
-        cuts = __shfl_sync(0xffffffffu, cuts, 0);
-      }
-      seq += kVBlocks + (more ? kKBlocks : 0);
-      if (more) more = ahead.next();
       if (ok && !leader && walk.last()) {
-        ok = mbar_wait_warp(&o_free, uint32_t(walk.item_no) & 1u, ctl, 14);
+        ok = wait_warp(&o_free, uint32_t(walk.item_no) & 1u, waits, 15);
         if (ok && lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&o_free), 0));
       }
     }
@@ -721,129 +816,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     const int half = t >> 6, row = t & 63;  // key half (and latent half of O), head
     const uint32_t lanes = tmem_addr(tmem, (warp & 3) * 32, 0);
     float m = -INFINITY, l = 0.f;  // the row's maximum (log2 units), this half's sum
+    // score of a hidden key: times scale_log2 it is -infinity
+    const uint32_t hidden = scale_log2 < 0.f ? 0x7f800000u : 0xff800000u;
     bool ok = true;
     for (int g = 0; walk.next(); ++g) {
       const Item& it = walk.it;
       const int node = 2 * it.pair + int(rank);
-      const bool live = node < it.r.nodes;
-      const uint32_t* mask =
-          a.tree_mask && live ? a.tree_mask + size_t(it.r.start + node) * a.mask_words : nullptr;
+      const bool live = node < it.r.nodes;  // (the same for the whole CTA)
       if (walk.first()) {
         m = -INFINITY;
         l = 0.f;
       }
-      // which of this thread's 128 keys the node sees
-      const int k0 = walk.tile * kTileKeys + half * 128;
-      uint32_t see[4];
-      {
-        const int n_pg = 128 >> a.page_shift;  // pages in the range, 1 .. 8
-        bool has = false;
-        if (lane < n_pg && k0 + (lane << a.page_shift) < it.r.keys)
-          has = page_of(a, walk.b, k0 + (lane << a.page_shift)) >= 0;
-        const uint32_t pages = __ballot_sync(0xffffffffu, has);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          see[w] = live ? seen_keys(a, it.r, mask, node, k0 + 32 * w) : 0u;
-          if (a.page_shift == 4) {
-            if (!((pages >> (2 * w)) & 1u)) see[w] &= 0xffff0000u;
-            if (!((pages >> (2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
-          } else if (!((pages >> ((32 * w) >> a.page_shift)) & 1u)) {
-            see[w] = 0u;
-          }
-        }
-      }
-      const bool all = (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu;
+      const int k0 = walk.tile * kTileKeys + half * 128;  // this thread's 128 keys
+      const int n_pg = 128 >> a.page_shift;               // pages in the range, 1 .. 8
+      bool has = false;
+      if (lane < n_pg && k0 + (lane << a.page_shift) < it.r.keys)
+        has = page_of(a, walk.b, k0 + (lane << a.page_shift)) >= 0;
+      const uint32_t pages = __ballot_sync(0xffffffffu, has);
       // After a wait that gave up (ok false) a warp goes on without waiting, so
       // that it meets the others at the named barriers, until all leave together.
-      if (test_stall && rank == 0 && blockIdx.x == 0) ok = mbar_wait_warp(&never_bar, 0, ctl, 30);
-      ok = ok && mbar_wait_warp(&s_full[g & 1], uint32_t(g >> 1) & 1u, ctl, 20);
+      if (test_stall && rank == 0 && blockIdx.x == 0) ok = wait_warp(&never_bar, 0, waits, 30);
+      ok = ok && wait_warp(&s_full[g & 1], uint32_t(g >> 1) & 1u, waits, 20);
       tc_fence_after();
       const uint32_t sc = lanes + kColS + 128u * uint32_t(g & 1);
+      float mt = -INFINITY;
+      if (live) {
+        if (k0 + 128 > it.r.ctx || pages != (1u << n_pg) - 1u) {
+          // hide what the node does not see
+          const uint32_t* mask =
+              a.tree_mask ? a.tree_mask + size_t(it.r.start + node) * a.mask_words : nullptr;
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {
+            uint32_t see = seen_keys(a, it.r, mask, node, k0 + 32 * w);
+            if (a.page_shift == 4) {
+              if (!((pages >> (2 * w)) & 1u)) see &= 0xffff0000u;
+              if (!((pages >> (2 * w + 1)) & 1u)) see &= 0x0000ffffu;
+            } else if (!((pages >> ((32 * w) >> a.page_shift)) & 1u)) {
+              see = 0u;
+            }
+            uint32_t r[32];
+            tmem_ld32(sc + 32 * w, r);
+            tmem_ld_wait();
+            reg_fence(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = (see >> i) & 1u ? r[i] : hidden;
+            tmem_st32(sc + 32 * w, r);
+          }
+          tmem_st_wait();
+        }
+        // the maximum of this half
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w) {
+          uint32_t r[32];
+          tmem_ld32(sc + 32 * w, r);
+          tmem_ld_wait();
+          reg_fence(r);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mt = fmax3(mt, __uint_as_float(r[i]) * scale_log2, __uint_as_float(r[i + 1]) * scale_log2);
+        }
+      }
+      xch[g & 1][half][row] = mt;
+      if (!named_barrier_and(1, 128, ok)) break;  // all 128 threads together
+      mt = fmaxf(mt, xch[g & 1][half ^ 1][row]);
+      // The maximum in use stays until a score passes it by more than 8 (then
+      // the exponentials reach 2^8): O is seldom rescaled.
+      float alpha = 1.f;
+      if (mt > m + kRescale || m == -INFINITY) {
+        if (m != -INFINITY) alpha = fast_exp2(m - mt);
+        m = mt;
+      }
+      const float mx = m == -INFINITY ? 0.f : m;
       uint32_t pk[64];
-      float acc[4];
-      // P of all 128 keys against the maximum `mx`; sums in acc
-      auto exponentials = [&](float mx) {
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      if (live) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t r[32];
           tmem_ld32(sc + 32 * w, r);
           tmem_ld_wait();
           reg_fence(r);
-          if (all) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x0 = fmaf(__uint_as_float(r[2 * i]), scale_log2, -mx);
-              const float x1 = fmaf(__uint_as_float(r[2 * i + 1]), scale_log2, -mx);
-              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-              acc[2 * (i & 1)] += p0;
-              acc[2 * (i & 1) + 1] += p1;
-              pk[16 * w + i] = pack_bf16x2(p0, p1);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x0 = fmaf(__uint_as_float(r[2 * i]), scale_log2, -mx);
-              const float x1 = fmaf(__uint_as_float(r[2 * i + 1]), scale_log2, -mx);
-              const float p0 = (see[w] >> (2 * i)) & 1u ? fast_exp2(x0) : 0.f;
-              const float p1 = (see[w] >> (2 * i + 1)) & 1u ? fast_exp2(x1) : 0.f;
-              acc[2 * (i & 1)] += p0;
-              acc[2 * (i & 1) + 1] += p1;
-              pk[16 * w + i] = pack_bf16x2(p0, p1);
-            }
+          for (int i = 0; i < 16; ++i) {
+            float x0, x1;
+            ffma2(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scale_log2,
+                  scale_log2, -mx, -mx);
+            x0 = fast_exp2(x0);
+            x1 = fast_exp2(x1);
+            fadd2(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], acc[2 * (i & 1)], acc[2 * (i & 1) + 1],
+                  x0, x1);
+            pk[16 * w + i] = pack_bf16x2(x0, x1);
           }
         }
-      };
-      float alpha = 1.f;
-      // a pair's absent second node (the whole CTA): P = 0
-      const bool idle = !live && ok;
-      if (idle) {
+      } else {  // a pair's absent second node
 #pragma unroll
         for (int i = 0; i < 64; ++i) pk[i] = 0u;
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
       }
-      bool keep = ok && !walk.first() && m > -INFINITY;
-      if (idle) {
-        keep = true;
-      } else if (keep) {
-        exponentials(m);
-        keep = (acc[0] + acc[1]) + (acc[2] + acc[3]) <= 256.f;
-      }
-      if (!named_barrier_and(1, 128, keep)) {
-        // the exact maximum of the tile, over both halves of the row
-        float mt = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t r[32];
-          tmem_ld32(sc + 32 * w, r);
-          tmem_ld_wait();
-          reg_fence(r);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if ((see[w] >> i) & 1u) mt = fmaxf(mt, __uint_as_float(r[i]) * scale_log2);
-        }
-        xch[half][row] = mt;
-        named_barrier_sync(1, 128);
-        mt = fmaxf(mt, xch[half ^ 1][row]);
-        named_barrier_sync(1, 128);
-        if (m == -INFINITY || mt > m + kRescale) {
-          if (mt > -INFINITY) {
-            alpha = m == -INFINITY ? 1.f : fast_exp2(m - mt);
-            m = mt;
-          }
-        }
-        if (!named_barrier_and(1, 128, ok)) break;  // all 128 threads together
-        exponentials(m == -INFINITY ? 0.f : m);
-      }
-      __syncwarp();
       tc_fence_before();
+      __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[g & 1]);
       l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
       // O holds the products up to tile g - 1: rescale it once they are done.
       // Its halves of columns belong to different threads, all of one alpha
       // per row; alpha is 1 in an item's first tile.
       if (__any_sync(0xffffffffu, alpha != 1.f)) {
-        ok = mbar_wait_warp(&p_free[1], uint32_t(g - 1) & 1u, ctl, 21);
+        ok = wait_warp(&p_free[1], uint32_t(g - 1) & 1u, waits, 21);
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; ok && c < 8; ++c) {
@@ -863,7 +940,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       __syncwarp();
       if (ok && half == 1 && lane == 0) mbar_arrive(&p_full[0]);
       // P into shared memory once the value products have read the last tile's
-      if (ok && g > 0) ok = mbar_wait_warp(&p_free[half], uint32_t(g - 1) & 1u, ctl, 22);
+      if (ok && g > 0) ok = wait_warp(&p_free[half], uint32_t(g - 1) & 1u, waits, 22);
       uint8_t* pr = smem + kOffP + half * 2 * kQBlk + row * 128;
 #pragma unroll
       for (int u = 0; u < 16; ++u)
@@ -875,11 +952,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       if (!walk.last()) continue;
 
       // ---- epilogue of the item
-      xch[half][row] = l;
+      xsum[half][row] = l;
       named_barrier_sync(1, 128);
-      const float lsum = l + xch[half ^ 1][row];
-      named_barrier_sync(1, 128);
-      ok = ok && mbar_wait_warp(&p_free[1], uint32_t(g) & 1u, ctl, 23);
+      const float lsum = l + xsum[half ^ 1][row];
+      ok = ok && wait_warp(&p_free[1], uint32_t(g) & 1u, waits, 23);
       tc_fence_after();
       float* dst;
       float f = 1.f;
@@ -916,34 +992,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   __syncwarp();
   tc_fence_before();
   cluster_sync();
-  if (warp == 3 && lane == 0) {
+  if (warp == 9 && lane == 0 && n_cut[1] < n_cut[0]) {
     // cut blocks that were issued but not reported (after an abort): they land
     // on this CTA's barriers, then count on the even CTA's
     int zero = 0;
-    WaitCtl drain{&zero, wait_limit_ns, kErrKernelTree, err_word};
-    if (n_cut[1] < n_cut[0]) {
-      // issue order: the ring is the same for both CTAs, so is the position
-      uint32_t at = 0, cuts = 0;
-      Walk w(a, s, first_item, n_items, step), ahead = w;
-      uint32_t seq = 0;
-      bool more = ahead.next();
-      for (int g = 0; more && g < 2; ++g) {
-        seq += kKBlocks;
-        more = ahead.next();
-      }
-      while (cuts < n_cut[0] && w.next()) {
-        for (int i = 0; i < kVBlocks && cuts < n_cut[0]; ++i) {
-          if (w.cut(i >> 1, box_rows) < 0) continue;
-          at = seq + (more ? 2 * i + 1 : i);
-          if (cuts >= n_cut[1]) {
-            mbar_wait(&cut_full[i & 1], (cuts >> 1) & 1u, drain, 15);
-            mbar_complete_tx_cluster(mapa_shared(smem_u32(&full[at % kRing]), 0), kBlk);
-          }
-          ++cuts;
+    const Waits drain{&zero, err_word, wait_limit_ns};
+    Walk w(a, s, first_item, n_items, step);
+    uint32_t cuts = 0;
+    for (int g = 0; cuts < n_cut[0] && w.next(); ++g) {
+      const int cut = w.cut();
+      for (int k = 0; cut >= 0 && k < 2 && cuts < n_cut[0]; ++k, ++cuts)
+        if (cuts >= n_cut[1]) {
+          const uint32_t slot = (uint32_t(g) * kVBlocks + 2 * cut + k) % kVRing;
+          wait_more(&cut_full[k], (cuts >> 1) & 1u, drain, 16);
+          mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
         }
-        seq += kVBlocks + (more ? kKBlocks : 0);
-        if (more) more = ahead.next();
-      }
     }
   }
   __syncwarp();
@@ -952,11 +1015,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     // Account for blocks that only one CTA issued (possible only after an
     // abort), then wait for the last phase of every slot.
     int zero = 0;
-    WaitCtl drain{&zero, wait_limit_ns, kErrKernelTree, err_word};
-    for (int which = 0; which < 2; ++which) {
-      uint64_t* bars = which == 0 ? full : q_full;
-      const uint32_t ring = which == 0 ? kRing : kKBlocks;
-      const uint32_t bytes = which == 0 ? kBlk : kQBlk;
+    const Waits drain{&zero, err_word, wait_limit_ns};
+    for (int which = 0; which < 3; ++which) {
+      uint64_t* bars = which == 0 ? k_full : which == 1 ? v_full : q_full;
+      const uint32_t ring = which == 0 ? kKRing : which == 1 ? kVRing : kKBlocks;
+      const uint32_t bytes = which == 2 ? kQBlk : kBlk;
       const uint32_t own = n_issued[which];
       const uint32_t peer = ld_shared_cluster_u32(mapa_shared(smem_u32(&n_issued[which]), 1));
       const uint32_t lo = min(own, peer), hi = max(own, peer);
@@ -968,7 +1031,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
           mbar_arrive_expect_tx(fb, bytes);
       }
       for (uint32_t i = hi > ring ? hi - ring : 0; i < hi; ++i)
-        mbar_wait(&bars[i % ring], (i / ring) & 1u, drain, 16);
+        wait_more(&bars[i % ring], (i / ring) & 1u, drain, 17);
     }
   }
   // Last barrier: no copy is in flight toward either CTA; neither leaves, nor
@@ -982,13 +1045,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
 }
 
 // ---------------------------------------------------------------- value
-// out[n, h * 128 + e] = sum_r o~[n, h, r] V_h[e, r]: 16 tokens x 64 value dims
-// per CTA (grid: 64 heads * 2 halves, token tiles). The rows of o~ are joined
-// from the partial results of their request first.
+// out[n, h * 128 + e] = sum_r o~[n, h, r] V_h[e, r]: 16 tokens x kE value dims
+// a step. Grid (64 heads * 128 / kE, y): a CTA keeps its weights in shared
+// memory and walks every y-th token tile. The rows of o~ are joined from the
+// partial results of their request first, by one warp a row or, when there are
+// fewer rows than warps, by several that share the ranges.
 constexpr int kVTok = 16;
-constexpr int kVThreads = 256;
 constexpr int kVLd = kLat + 8;
-constexpr size_t kVSmem = size_t(2 * kVTok + 64) * kVLd * 2;
+constexpr size_t value_smem(int e) {
+  return size_t(2 * kVTok + e) * kVLd * 2 + size_t(e / 8) * kLat * 4;
+}
 
 // x as a bf16 and the bf16 of what it leaves: together 2^-17 of x, so that the
 // latent result loses nothing that the output's own rounding would show.
@@ -1000,110 +1066,152 @@ __device__ __forceinline__ void split_store(__nv_bfloat16* hi, __nv_bfloat16* lo
                  pack_bf16x2(x.z - __uint_as_float(h1 << 16), x.w - __uint_as_float(h1 & 0xffff0000u)));
 }
 
-__global__ void __launch_bounds__(kVThreads) tree_value_kernel(const AttnTreeArgs a, const Scratch s) {
+// Row n's latent result of head h: its columns 4 (32 c + lane) .. + 3 for c =
+// 0..3, over the ranges j, j + ways, ...; false for a row of no request.
+__device__ __forceinline__ bool join_row(const AttnTreeArgs& a, const Scratch& s, int n, int h, int j,
+                                         int ways, int lane, float4 (&acc)[4]) {
+  const TreeReq r = s.req[s.row_req[n]];
+  const int node = n - r.start;
+  if (node < 0 || node >= r.nodes) return false;
+  if (r.ranges <= 1) {
+    const float4* src = reinterpret_cast<const float4*>(s.o + (size_t(n) * kHeads + h) * kLat);
+    if (r.tiles > 0 && j == 0)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] = src[c * 32 + lane];
+    return true;
+  }
+  const size_t pairs = size_t(r.nodes + 1) / 2;
+  const size_t prow = size_t(r.slot + node / 2) * 128 + (node & 1) * 64 + h;
+  float mx = -INFINITY;
+  for (int k = lane; k < r.ranges; k += 32) mx = fmaxf(mx, s.part_ml[prow + k * pairs * 128].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  if (mx == -INFINITY) return true;  // nothing visible: zeros
+  float sum = 0.f;
+  for (int k = lane; k < r.ranges; k += 32) {
+    const float2 ml = s.part_ml[prow + k * pairs * 128];
+    sum = fmaf(exp2f(ml.x - mx), ml.y, sum);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const float inv = 1.f / sum;
+#pragma unroll 4
+  for (int k = j; k < r.ranges; k += ways) {
+    const size_t pr = prow + k * pairs * 128;
+    const float f = exp2f(s.part_ml[pr].x - mx) * inv;
+    const float4* src = reinterpret_cast<const float4*>(s.part_o + pr * kLat);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 v = src[c * 32 + lane];
+      acc[c].x = fmaf(f, v.x, acc[c].x);
+      acc[c].y = fmaf(f, v.y, acc[c].y);
+      acc[c].z = fmaf(f, v.z, acc[c].z);
+      acc[c].w = fmaf(f, v.w, acc[c].w);
+    }
+  }
+  return true;
+}
+
+template <int kE>
+__global__ void __launch_bounds__(kE * 4)
+    tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s) {
+  constexpr int kThreads = kE * 4, kWarps = kE / 8, kSplit = 128 / kE;
   extern __shared__ __align__(16) uint8_t smem[];
   auto* so = reinterpret_cast<__nv_bfloat16*>(smem);
   auto* sl = so + kVTok * kVLd;
   auto* sw = sl + kVTok * kVLd;
+  auto* part = reinterpret_cast<float4*>(sw + kE * kVLd);  // [warps][128]
   __shared__ int live[kVTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x >> 1, e0 = (blockIdx.x & 1) * 64;
-  const int n0 = blockIdx.y * kVTok;
+  const int h = blockIdx.x / kSplit, e0 = blockIdx.x % kSplit * kE;
   const auto* w =
       static_cast<const __nv_bfloat16*>(a.w_kv_b) + (size_t(h) * 256 + kNope + e0) * kLat;
-  for (int i = tid; i < 64 * (kLat / 8); i += kVThreads) {
+  for (int i = tid; i < kE * (kLat / 8); i += kThreads) {
     const int e = i / (kLat / 8), c = i % (kLat / 8) * 8;
     cp16(smem_u32(sw + e * kVLd + c), w + size_t(e) * kLat + c, true);
   }
   cp_commit();
-  // two tokens per warp
-  for (int q = warp; q < kVTok; q += kVThreads / 32) {
-    const int n = n0 + q;
-    float4 acc[4] = {};
-    bool ok = false;
-    if (n < a.N) {
-      int l = 0, hi = a.B;  // the last request that starts at or before row n
-      while (hi - l > 1) {
-        const int mid = (l + hi) >> 1;
-        if (a.cu_new[mid] <= n) l = mid;
-        else hi = mid;
+  const int tiles = (a.N + kVTok - 1) / kVTok;
+  for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+    const int n0 = tile * kVTok;
+    const int rows = min(kVTok, a.N - n0);
+    const int ways = max(kWarps / rows, 1);
+    if (ways == 1) {
+      for (int q = warp; q < kVTok; q += kWarps) {
+        float4 acc[4] = {};
+        const bool ok = q < rows && join_row(a, s, n0 + q, h, 0, 1, lane, acc);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int at = q * kVLd + (c * 32 + lane) * 4;
+          split_store(so + at, sl + at, acc[c]);
+        }
+        if (lane == 0) live[q] = ok;
       }
-      const TreeReq r = s.req[l];
-      const int node = n - r.start;
-      ok = node >= 0 && node < r.nodes;
-      if (ok && r.ranges <= 1) {
-        const float4* src = reinterpret_cast<const float4*>(s.o + (size_t(n) * kHeads + h) * kLat);
-        if (r.tiles > 0)
+    } else {
+      const int q = warp / ways, j = warp % ways;
+      float4 acc[4] = {};
+      const bool ok = q < rows && join_row(a, s, n0 + q, h, j, ways, lane, acc);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[c] = src[c * 32 + lane];
-      } else if (ok) {
-        const int pairs = (r.nodes + 1) / 2;
-        const size_t prow = size_t(r.slot + node / 2) * 128 + (node & 1) * 64 + h;
-        float mx = -INFINITY;
-        for (int k = 0; k < r.ranges; ++k)
-          mx = fmaxf(mx, s.part_ml[prow + size_t(k) * pairs * 128].x);
-        float sum = 0.f;
-        if (mx > -INFINITY)
-          for (int k = 0; k < r.ranges; ++k) {
-            const size_t pr = prow + size_t(k) * pairs * 128;
-            const float2 ml = s.part_ml[pr];
-            const float f = exp2f(ml.x - mx);
-            sum = fmaf(f, ml.y, sum);
-            const float4* src = reinterpret_cast<const float4*>(s.part_o + pr * kLat);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float4 v = src[c * 32 + lane];
-              acc[c].x = fmaf(f, v.x, acc[c].x);
-              acc[c].y = fmaf(f, v.y, acc[c].y);
-              acc[c].z = fmaf(f, v.z, acc[c].z);
-              acc[c].w = fmaf(f, v.w, acc[c].w);
-            }
+      for (int c = 0; c < 4; ++c) part[warp * 128 + c * 32 + lane] = acc[c];
+      if (j == 0 && lane == 0 && q < rows) live[q] = ok;
+      __syncthreads();
+      for (int i = tid; i < kVTok * 128; i += kThreads) {
+        const int qq = i >> 7, c = i & 127;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (qq < rows)
+          for (int k = 0; k < ways; ++k) {
+            const float4 y = part[(qq * ways + k) * 128 + c];
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
           }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          acc[c] = make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv);
+        split_store(so + qq * kVLd + c * 4, sl + qq * kVLd + c * 4, x);
+        if (c == 0 && qq >= rows) live[qq] = 0;
       }
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int at = q * kVLd + (c * 32 + lane) * 4;
-      split_store(so + at, sl + at, acc[c]);
-    }
-    if (lane == 0) live[q] = ok;
-  }
-  cp_wait<0>();
-  __syncthreads();
-  float d[4] = {};
+    cp_wait<0>();
+    __syncthreads();
+    float d[4] = {};
 #pragma unroll 4
-  for (int k = 0; k < kLat / 16; k += 2) {
-    uint32_t fa[4], fb[4];
-    // one ldmatrix gives this warp's 8 value dims for two 16-wide steps
-    ldsm4(fb, smem_u32(sw + (warp * 8 + (lane & 7)) * kVLd + k * 16 + (lane >> 3) * 8));
+    for (int k = 0; k < kLat / 16; k += 2) {
+      uint32_t fa[4], fb[4];
+      // one ldmatrix gives this warp's 8 value dims for two 16-wide steps
+      ldsm4(fb, smem_u32(sw + (warp * 8 + (lane & 7)) * kVLd + k * 16 + (lane >> 3) * 8));
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int at = (lane & 15) * kVLd + (k + j) * 16 + (lane >> 4) * 8;
-      ldsm4(fa, smem_u32(so + at));
-      mma_16816(d, fa, fb[2 * j], fb[2 * j + 1]);
-      ldsm4(fa, smem_u32(sl + at));
-      mma_16816(d, fa, fb[2 * j], fb[2 * j + 1]);
+      for (int i = 0; i < 2; ++i) {
+        const int at = (lane & 15) * kVLd + (k + i) * 16 + (lane >> 4) * 8;
+        ldsm4(fa, smem_u32(so + at));
+        mma_16816(d, fa, fb[2 * i], fb[2 * i + 1]);
+        ldsm4(fa, smem_u32(sl + at));
+        mma_16816(d, fa, fb[2 * i], fb[2 * i + 1]);
+      }
     }
-  }
-  const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int q = g + 8 * half;
-    if (live[q])
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                   size_t(n0 + q) * (kHeads * kVal) + h * kVal + e0 + warp * 8 +
-                                   2 * t) = pack_bf16x2(d[2 * half], d[2 * half + 1]);
+    for (int half = 0; half < 2; ++half) {
+      const int q = g + 8 * half;
+      if (live[q])
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
+                                     size_t(n0 + q) * (kHeads * kVal) + h * kVal + e0 + warp * 8 +
+                                     2 * t) = pack_bf16x2(d[2 * half], d[2 * half + 1]);
+    }
+    __syncthreads();  // the row buffers are written again
   }
+}
+
+template <int kE>
+cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int y, cudaStream_t stream) {
+  static ContextCache attr;
+  auto kern = tree_value_kernel<kE>;
+  const cudaError_t e =
+      ensure_smem_attr(reinterpret_cast<const void*>(kern), int(value_smem(kE)), &attr);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(kHeads * 128 / kE, unsigned(y)), kE * 4, value_smem(kE), stream>>>(a, s);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t attn_tree_scratch_bytes(int B, int64_t N) {
-  return 256 + up256(size_t(B) * sizeof(TreeReq)) + up256(size_t(N) * kHeads * kRow * 2) +
+  return 256 + up256(size_t(B) * sizeof(TreeReq)) + up256(size_t(N) * 4) + up256(size_t(N) * kHeads * kRow * 2) +
          up256(size_t(N) * kHeads * kLat * 4) + up256(size_t(kMaxSlots) * 128 * sizeof(float2)) +
          size_t(kMaxSlots) * 128 * kLat * 4;
 }
@@ -1125,26 +1233,25 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
       !encode_tmap_bf16(&tmC, a.cache, 3, c_dims, c_strides, c_box, true))
     return cudaErrorInvalidValue;
   const int tiles = (a.N + kQTok - 1) / kQTok;
-  const dim3 qgrid(kHeads * 4, unsigned(tiles) + 1);
+  const dim3 qgrid(kHeads * 4, unsigned(tiles < 3 ? tiles : 3) + 1);
   if (rotary)
-    tree_query_kernel<true><<<qgrid, kQThreads, 0, stream>>>(a, s, *rotary, clusters);
+    tree_query_kernel<true><<<qgrid, kQThreads, 0, stream>>>(a, s, *rotary, clusters, err_word);
   else
-    tree_query_kernel<false><<<qgrid, kQThreads, 0, stream>>>(a, s, RopeFreqs{}, clusters);
+    tree_query_kernel<false><<<qgrid, kQThreads, 0, stream>>>(a, s, RopeFreqs{}, clusters, err_word);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  static ContextCache attn_attr, value_attr;
+  float scale_log2 = a.scale * 1.4426950408889634f;
+  if (scale_log2 == 0.f) scale_log2 = std::numeric_limits<float>::min();  // see `hidden`
+  static ContextCache attn_attr;
   e = ensure_smem_attr(reinterpret_cast<const void*>(tree_attn_kernel), int(kASmem), &attn_attr);
   if (e != cudaSuccess) return e;
   tree_attn_kernel<<<2 * clusters, kAThreads, kASmem, stream>>>(
-      tmQ, tmC, a, s, a.scale * 1.4426950408889634f, box_rows, wait_limit_ns, err_word,
+      tmQ, tmC, a, s, scale_log2, wait_limit_ns, err_word,
       test_stall);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = ensure_smem_attr(reinterpret_cast<const void*>(tree_value_kernel), int(kVSmem), &value_attr);
-  if (e != cudaSuccess) return e;
-  tree_value_kernel<<<dim3(kHeads * 2, unsigned((a.N + kVTok - 1) / kVTok)), kVThreads, kVSmem,
-                      stream>>>(a, s);
-  return cudaGetLastError();
+  return a.N <= 2 * kVTok ? launch_value<64>(a, s, tiles, stream)
+                          : launch_value<128>(a, s, tiles < 2 ? tiles : 2, stream);
 }
 
 }  // namespace mla

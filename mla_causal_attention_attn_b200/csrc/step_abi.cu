@@ -133,8 +133,8 @@ mla_status_t mla_attn_tree(const mla_bf16* q_nope, const mla_bf16* q_pe, const m
   s = check_device();
   if (s != MLA_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  unsigned int* err = call_status_word(workspace, st, &s);
-  if (s != MLA_OK) return s;
+  // (the first kernel clears the call's status word)
+  unsigned int* err = static_cast<unsigned int*>(workspace);
   AttnTreeArgs a{q_nope,      q_pe,   W_kv_b,    rope ? positions : nullptr,
                  cache,       block_table, context_len, cu_new,
                  tree_mask,   out,    page_stride, B,
