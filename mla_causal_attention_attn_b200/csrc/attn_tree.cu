@@ -32,33 +32,31 @@ constexpr int kRow = 576;   // latent + rotary
 constexpr int kVal = 128;
 constexpr int kTileKeys = 256;
 constexpr int kMaxClusters = 74;               // two SMs each
-constexpr int kMaxSlots = 2 * kMaxClusters;    // see schedule()
+constexpr int kMaxSlots = 2 * kMaxClusters;    // see Share
 
 // ---------------------------------------------------------------- schedule
 // Request b with n nodes takes pairs = ceil(n / 2) node pairs and tiles =
-// ceil(keys / 256) key tiles, W = sum pairs * tiles tile visits in all. With
-// chunk = ceil(W / clusters), a request is split into ceil(tiles / chunk) even
-// ranges; its items are (range, pair), pairs fastest, so that neighbouring
-// clusters read the same keys at the same time. Only a split request
-// (tiles > chunk) needs partial results: it has pairs * ranges <= 2 * pairs *
-// tiles / chunk of them, 2 * W / chunk <= 2 * clusters over all requests.
+// ceil(keys / 256) key tiles. All (request, pair, tile) in that order, W in
+// all, are cut into equal shares: cluster c of C <= W takes [c W / C, (c+1) W / C).
+// A share begins and ends anywhere, so a pair's tiles may lie in several
+// shares; then each leaves a partial result, of which a cluster has at most
+// two: slot 2 c for its share's first piece, 2 c + 1 for its last. A pair that
+// lies in one share is written whole.
 struct TreeReq {
-  int start, nodes;    // first row, number of rows
-  int ctx, keys;       // cached keys before the nodes, keys in all
-  int tiles, ranges;
-  int slot;            // first partial slot, when ranges > 1
+  int start, nodes;  // first row, number of rows
+  int ctx, keys;     // cached keys before the nodes, keys in all
+  int tiles;
   int pad;
-  long long item;      // first item
-  long long pad2;
+  long long base;    // the request's first tile in the order above
 };
-static_assert(sizeof(TreeReq) == 48, "TreeReq");
+static_assert(sizeof(TreeReq) == 32, "TreeReq");
 
 struct Scratch {
-  long long* n_items;
+  long long* total;    // W
   TreeReq* req;        // [B]
   int* row_req;        // [N]: the last request that starts at or before the row
   __nv_bfloat16* q;    // [N, 64, 576]
-  float* o;            // [N, 64, 512], requests in one range
+  float* o;            // [N, 64, 512], pairs in one share
   float* part_o;       // [kMaxSlots][128][512]
   float2* part_ml;     // [kMaxSlots][128] running maximum (log2 units) and sum
 };
@@ -68,7 +66,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 Scratch carve(void* base, int B, int64_t N) {
   uint8_t* p = static_cast<uint8_t*>(base);
   Scratch s;
-  s.n_items = reinterpret_cast<long long*>(p);
+  s.total = reinterpret_cast<long long*>(p);
   p += 256;
   s.req = reinterpret_cast<TreeReq*>(p);
   p += up256(size_t(B) * sizeof(TreeReq));
@@ -84,84 +82,70 @@ Scratch carve(void* base, int B, int64_t N) {
   return s;
 }
 
-// A request's lengths, made safe: rows inside [0, N], keys inside its table.
-__device__ __forceinline__ TreeReq read_request(const AttnTreeArgs& a, int b) {
-  TreeReq r{};
-  r.start = min(max(a.cu_new[b], 0), a.N);
-  r.nodes = min(max(a.cu_new[b + 1], r.start), a.N) - r.start;
-  const long long cap = min((long long)a.max_pages << a.page_shift, 0x7fffff00LL);
-  r.ctx = int(min((long long)max(a.context_len[b], 0), cap));
-  r.keys = int(min((long long)r.ctx + r.nodes, cap));
-  r.tiles = r.nodes > 0 ? (r.keys + kTileKeys - 1) / kTileKeys : 0;
-  return r;
-}
-
-// Block-wide exclusive scan of two 64-bit numbers (one pair per thread);
-// returns the totals through t0, t1.
-__device__ __forceinline__ void scan2(long long& x, long long& y, long long& t0, long long& t1,
-                                      long long (*warp_sum)[2]) {
+// Lays the requests out (one CTA). Lengths are made safe: rows inside [0, N]
+// and, by a running maximum of the starts, in one request at most; keys inside
+// the request's table.
+__device__ void schedule(const AttnTreeArgs& a, const Scratch& s) {
+  __shared__ long long warp_sum[8];
+  __shared__ int warp_max[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  long long ix = x, iy = y;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long ox = __shfl_up_sync(0xffffffffu, ix, d), oy = __shfl_up_sync(0xffffffffu, iy, d);
-    if (lane >= d) {
-      ix += ox;
-      iy += oy;
-    }
-  }
-  __syncthreads();
-  if (lane == 31) {
-    warp_sum[warp][0] = ix;
-    warp_sum[warp][1] = iy;
-  }
-  __syncthreads();
-  long long bx = 0, by = 0;
-  t0 = t1 = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w == warp) {
-      bx = t0;
-      by = t1;
-    }
-    t0 += warp_sum[w][0];
-    t1 += warp_sum[w][1];
-  }
-  x = bx + ix - x;
-  y = by + iy - y;
-}
-
-__device__ void schedule(const AttnTreeArgs& a, const Scratch& s, int clusters) {
-  __shared__ long long warp_sum[8][2];
-  long long visits = 0;
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-    const TreeReq r = read_request(a, b);
-    visits += (long long)((r.nodes + 1) / 2) * r.tiles;
-  }
-  long long zero = 0, total, t1;
-  scan2(visits, zero, total, t1, warp_sum);
-  const long long chunk = max((total + clusters - 1) / clusters, 1LL);
-  long long items = 0, slots = 0;
+  const int cap = int(min((long long)a.max_pages << a.page_shift, 0x7fffff00LL));
+  long long base = 0;
+  int top = 0;
   for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
+    int start = b < a.B ? min(max(a.cu_new[b], 0), a.N) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, start, d);
+      if (lane >= d) start = max(start, o);
+    }
+    __syncthreads();
+    if (lane == 31) warp_max[warp] = start;
+    __syncthreads();
+    for (int w = 0; w < warps; ++w) {
+      if (w == warp) start = max(start, top);
+      top = max(top, warp_max[w]);
+    }
     TreeReq r{};
-    long long x = 0, y = 0;
     if (b < a.B) {
-      r = read_request(a, b);
-      const int pairs = (r.nodes + 1) / 2;
-      r.ranges = int((r.tiles + chunk - 1) / chunk);
-      x = (long long)pairs * r.ranges;
-      y = r.ranges > 1 ? x : 0;
+      r.start = start;
+      r.nodes = max(min(a.cu_new[b + 1], a.N) - start, 0);
+      r.ctx = min(max(a.context_len[b], 0), cap);
+      r.keys = int(min((long long)r.ctx + r.nodes, (long long)cap));
+      r.tiles = r.nodes > 0 ? (r.keys + kTileKeys - 1) / kTileKeys : 0;
     }
-    scan2(x, y, total, t1, warp_sum);
-    if (b < a.B) {
-      r.item = items + x;
-      r.slot = int(slots + y);
-      s.req[b] = r;
+    const long long x = (long long)((r.nodes + 1) / 2) * r.tiles;
+    long long inc = x;  // inclusive scan over the block
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += o;
     }
-    items += total;
-    slots += t1;
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    long long before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w == warp) before = all;
+      all += warp_sum[w];
+    }
+    r.base = base + before + inc - x;
+    if (b < a.B) s.req[b] = r;
+    base += all;
   }
-  if (threadIdx.x == 0) *s.n_items = items;
+  if (threadIdx.x == 0) *s.total = base;
+}
+
+// Shares there are (none empty), the first position of share c, and the share
+// of position p.
+__device__ __forceinline__ int shares(long long total, int clusters) {
+  return int(min((long long)clusters, total));
+}
+__device__ __forceinline__ long long share_begin(long long total, int c, int clusters) {
+  return total * c / clusters;
+}
+__device__ __forceinline__ int share_of(long long total, long long p, int clusters) {
+  return int(((p + 1) * clusters - 1) / total);
 }
 
 // ---------------------------------------------------------------- fragments
@@ -260,11 +244,11 @@ __device__ void rotate_queries(const AttnTreeArgs& a, const Scratch& s, const Ro
 template <bool kRope>
 __global__ void __launch_bounds__(kQThreads)
     tree_query_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
-                      const __grid_constant__ RopeFreqs f, int clusters, unsigned int* err_word) {
+                      const __grid_constant__ RopeFreqs f, unsigned int* err_word) {
   if (blockIdx.y == gridDim.y - 1) {
     if (blockIdx.x == 0) {
       if (threadIdx.x == 0) *err_word = 0u;
-      schedule(a, s, clusters);
+      schedule(a, s);
     } else {
       rotate_queries<kRope>(a, s, f, blockIdx.x - 1, gridDim.x - 1);
     }
@@ -323,33 +307,6 @@ __global__ void __launch_bounds__(kQThreads)
 }
 
 // ---------------------------------------------------------------- attention
-// The item's request, pair and key-tile range.
-struct Item {
-  TreeReq r;
-  int pair, range, t0, t1;
-};
-
-__device__ __forceinline__ Item find_item(const AttnTreeArgs& a, const Scratch& s, long long i,
-                                          int& b) {
-  int l = 0, h = a.B;  // the last request whose first item is at or before i
-  while (h - l > 1) {
-    const int m = (l + h) >> 1;
-    if (s.req[m].item <= i) l = m;
-    else h = m;
-  }
-  Item it;
-  b = l;
-  it.r = s.req[l];
-  const int pairs = (it.r.nodes + 1) / 2;
-  const int k = int(i - it.r.item);
-  it.range = k / pairs;
-  it.pair = k % pairs;
-  // (ranges <= clusters, so the products stay below 2^31)
-  it.t0 = int(unsigned(it.r.tiles) * unsigned(it.range) / unsigned(it.r.ranges));
-  it.t1 = int(unsigned(it.r.tiles) * unsigned(it.range + 1) / unsigned(it.r.ranges));
-  return it;
-}
-
 // The page holding key j of a request, or -1.
 __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
   const int id = a.block_table[size_t(b) * size_t(a.max_pages) + (j >> a.page_shift)];
@@ -407,43 +364,63 @@ static_assert(kASmem <= 225 * 1024, "shared memory budget");
 constexpr uint32_t kColO = 0, kColS = 256;       // tensor memory columns
 constexpr float kRescale = 8.f;                  // log2 growth of the maximum that rescales O
 
-// What a cluster visits: its items one after another, tile by tile.
+// What a cluster visits: the items (pieces of pairs) of its share, tile by tile.
 struct Walk {
   const AttnTreeArgs* a;
   const Scratch* s;
-  long long next_item, n_items, step;
-  Item it;
-  int b, tile;
+  long long pos, end;  // the next item's first position, the share's end
+  TreeReq r;
+  int b, pair, tile, t0, t1;
+  int slot;      // of the item's partial result, or -1: the pair is whole
+  int next_slot;
   int item_no;   // items begun so far - 1
   int cut_last;  // cut chunk of the item's last tile, or -1
   int cut_row;   // its first row without a key
 
-  __device__ __forceinline__ Walk(const AttnTreeArgs& aa, const Scratch& ss, long long first,
-                                  long long n, long long st)
-      : a(&aa), s(&ss), next_item(first), n_items(n), step(st), item_no(-1) {
-    it.t1 = 0;
-    tile = 0;
+  __device__ __forceinline__ Walk(const AttnTreeArgs& aa, const Scratch& ss, int cluster,
+                                  int clusters)
+      : a(&aa), s(&ss), tile(0), t1(0), next_slot(2 * cluster), item_no(-1) {
+    const long long total = *ss.total;
+    clusters = shares(total, clusters);
+    pos = end = 0;
+    if (cluster < clusters) {
+      pos = share_begin(total, cluster, clusters);
+      end = share_begin(total, cluster + 1, clusters);
+    }
   }
   // Moves to the next tile; false at the end.
   __device__ __forceinline__ bool next() {
-    if (item_no >= 0 && ++tile < it.t1) return true;
-    if (next_item >= n_items) return false;
-    it = find_item(*a, *s, next_item, b);
-    tile = it.t0;
-    next_item += step;
+    if (item_no >= 0 && ++tile < t1) return true;
+    if (pos >= end) return false;
+    int h = a->B;  // the last request whose first position is at or before pos
+    b = 0;
+    while (h - b > 1) {
+      const int m = (b + h) >> 1;
+      if (s->req[m].base <= pos) b = m;
+      else h = m;
+    }
+    r = s->req[b];
+    const long long rel = pos - r.base;
+    pair = int(rel / r.tiles);
+    t0 = int(rel - (long long)pair * r.tiles);
+    t1 = int(min((long long)r.tiles, t0 + (end - pos)));
+    tile = t0;
+    pos += t1 - t0;
+    slot = t0 == 0 && t1 == r.tiles ? -1 : next_slot;
+    next_slot |= 1;
     ++item_no;
     // The chunk of 64 keys that the request's last key lies in has rows to be
     // zeroed when a TMA box (min(page, 64) rows) goes past that key.
     const int box = a->page_shift >= 6 ? 64 : 1 << a->page_shift;
     cut_last = -1;
-    if (it.t1 == it.r.tiles && (it.r.keys & (box - 1)) != 0) {
-      cut_last = ((it.r.keys - 1) & (kTileKeys - 1)) >> 6;
-      cut_row = it.r.keys & 63;
+    if (t1 == r.tiles && (r.keys & (box - 1)) != 0) {
+      cut_last = ((r.keys - 1) & (kTileKeys - 1)) >> 6;
+      cut_row = r.keys & 63;
     }
     return true;
   }
-  __device__ __forceinline__ bool first() const { return tile == it.t0; }
-  __device__ __forceinline__ bool last() const { return tile + 1 == it.t1; }
+  __device__ __forceinline__ bool first() const { return tile == t0; }
+  __device__ __forceinline__ bool last() const { return tile + 1 == t1; }
   // The tile's chunk with rows to be zeroed, or -1.
   __device__ __forceinline__ int cut() const { return last() ? cut_last : -1; }
 };
@@ -588,9 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   cluster_sync();  // both CTAs' barriers are initialised before any remote signal
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const long long n_items = *s.n_items;
-  const long long first_item = blockIdx.x >> 1, step = gridDim.x >> 1;
-  Walk walk(a, s, first_item, n_items, step);
+  Walk walk(a, s, int(blockIdx.x >> 1), int(gridDim.x >> 1));
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers
@@ -605,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     const int per = 64 >> box_shift;  // boxes a 64-key chunk
     const int pmask = (1 << a.page_shift) - 1;
     auto page_at = [&](int key) -> int {  // page, or one past the last: zeros
-      const int id = key < walk.it.r.keys ? page_of(a, walk.b, key) : -1;
+      const int id = key < walk.r.keys ? page_of(a, walk.b, key) : -1;
       return id >= 0 ? id : a.num_pages;
     };
     uint32_t issued = 0;
@@ -619,9 +594,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         const int key = walk.tile * kTileKeys + int(rank) * 128 + (lane << box_shift);
         const int page = lane < 2 * per ? page_at(key) : 0;
         const bool first = walk.first();
-        const int node = 2 * walk.it.pair + int(rank);
+        const int node = 2 * walk.pair + int(rank);
         const int qrow =
-            node < walk.it.r.nodes ? (walk.it.r.start + node) * kHeads : a.N * kHeads;  // zeros
+            node < walk.r.nodes ? (walk.r.start + node) * kHeads : a.N * kHeads;  // zeros
 #pragma unroll 1
         for (int i = 0; ok && i < kKBlocks; ++i) {
           if (first) {
@@ -820,9 +795,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     const uint32_t hidden = scale_log2 < 0.f ? 0x7f800000u : 0xff800000u;
     bool ok = true;
     for (int g = 0; walk.next(); ++g) {
-      const Item& it = walk.it;
-      const int node = 2 * it.pair + int(rank);
-      const bool live = node < it.r.nodes;  // (the same for the whole CTA)
+      const int node = 2 * walk.pair + int(rank);
+      const bool live = node < walk.r.nodes;  // (the same for the whole CTA)
       if (walk.first()) {
         m = -INFINITY;
         l = 0.f;
@@ -830,7 +804,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       const int k0 = walk.tile * kTileKeys + half * 128;  // this thread's 128 keys
       const int n_pg = 128 >> a.page_shift;               // pages in the range, 1 .. 8
       bool has = false;
-      if (lane < n_pg && k0 + (lane << a.page_shift) < it.r.keys)
+      if (lane < n_pg && k0 + (lane << a.page_shift) < walk.r.keys)
         has = page_of(a, walk.b, k0 + (lane << a.page_shift)) >= 0;
       const uint32_t pages = __ballot_sync(0xffffffffu, has);
       // After a wait that gave up (ok false) a warp goes on without waiting, so
@@ -841,13 +815,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       const uint32_t sc = lanes + kColS + 128u * uint32_t(g & 1);
       float mt = -INFINITY;
       if (live) {
-        if (k0 + 128 > it.r.ctx || pages != (1u << n_pg) - 1u) {
+        if (k0 + 128 > walk.r.ctx || pages != (1u << n_pg) - 1u) {
           // hide what the node does not see
           const uint32_t* mask =
-              a.tree_mask ? a.tree_mask + size_t(it.r.start + node) * a.mask_words : nullptr;
+              a.tree_mask ? a.tree_mask + size_t(walk.r.start + node) * a.mask_words : nullptr;
 #pragma unroll 1
           for (int w = 0; w < 4; ++w) {
-            uint32_t see = seen_keys(a, it.r, mask, node, k0 + 32 * w);
+            uint32_t see = seen_keys(a, walk.r, mask, node, k0 + 32 * w);
             if (a.page_shift == 4) {
               if (!((pages >> (2 * w)) & 1u)) see &= 0xffff0000u;
               if (!((pages >> (2 * w + 1)) & 1u)) see &= 0x0000ffffu;
@@ -959,14 +933,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       tc_fence_after();
       float* dst;
       float f = 1.f;
-      if (it.r.ranges > 1) {
-        const int pairs = (it.r.nodes + 1) / 2;
-        const size_t prow = size_t(it.r.slot + it.range * pairs + it.pair) * 128 + rank * 64 + row;
+      if (walk.slot >= 0) {
+        const size_t prow = size_t(walk.slot) * 128 + rank * 64 + row;
         if (half == 0 && live) s.part_ml[prow] = make_float2(m, lsum);
         dst = s.part_o + prow * kLat;
       } else {
         f = lsum > 0.f ? 1.f / lsum : 0.f;
-        dst = s.o + (size_t(it.r.start + node) * kHeads + row) * kLat;
+        dst = s.o + (size_t(walk.r.start + node) * kHeads + row) * kLat;
       }
 #pragma unroll 1
       for (int c = 0; ok && c < 8; ++c) {
@@ -997,7 +970,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     // on this CTA's barriers, then count on the even CTA's
     int zero = 0;
     const Waits drain{&zero, err_word, wait_limit_ns};
-    Walk w(a, s, first_item, n_items, step);
+    Walk w(a, s, int(blockIdx.x >> 1), int(gridDim.x >> 1));
     uint32_t cuts = 0;
     for (int g = 0; cuts < n_cut[0] && w.next(); ++g) {
       const int cut = w.cut();
@@ -1067,37 +1040,47 @@ __device__ __forceinline__ void split_store(__nv_bfloat16* hi, __nv_bfloat16* lo
 }
 
 // Row n's latent result of head h: its columns 4 (32 c + lane) .. + 3 for c =
-// 0..3, over the ranges j, j + ways, ...; false for a row of no request.
-__device__ __forceinline__ bool join_row(const AttnTreeArgs& a, const Scratch& s, int n, int h, int j,
+// 0..3, over the pieces j, j + ways, ... of its pair; false for a row of no
+// request.
+__device__ __forceinline__ bool join_row(const Scratch& s, int clusters, int n, int h, int j,
                                          int ways, int lane, float4 (&acc)[4]) {
   const TreeReq r = s.req[s.row_req[n]];
   const int node = n - r.start;
   if (node < 0 || node >= r.nodes) return false;
-  if (r.ranges <= 1) {
+  if (r.tiles == 0) return true;
+  const long long total = *s.total;
+  clusters = shares(total, clusters);
+  const long long p0 = r.base + (long long)(node >> 1) * r.tiles;
+  const int c0 = share_of(total, p0, clusters);
+  const int pieces = share_of(total, p0 + r.tiles - 1, clusters) - c0 + 1;
+  if (pieces == 1) {
     const float4* src = reinterpret_cast<const float4*>(s.o + (size_t(n) * kHeads + h) * kLat);
-    if (r.tiles > 0 && j == 0)
+    if (j == 0)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[c] = src[c * 32 + lane];
     return true;
   }
-  const size_t pairs = size_t(r.nodes + 1) / 2;
-  const size_t prow = size_t(r.slot + node / 2) * 128 + (node & 1) * 64 + h;
+  // row of piece k's partial result
+  const int first = 2 * c0 + (share_begin(total, c0, clusters) < p0 ? 1 : 0);
+  auto prow = [&](int k) {
+    return size_t(k == 0 ? first : 2 * (c0 + k)) * 128 + (node & 1) * 64 + h;
+  };
   float mx = -INFINITY;
-  for (int k = lane; k < r.ranges; k += 32) mx = fmaxf(mx, s.part_ml[prow + k * pairs * 128].x);
+  for (int k = lane; k < pieces; k += 32) mx = fmaxf(mx, s.part_ml[prow(k)].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   if (mx == -INFINITY) return true;  // nothing visible: zeros
   float sum = 0.f;
-  for (int k = lane; k < r.ranges; k += 32) {
-    const float2 ml = s.part_ml[prow + k * pairs * 128];
+  for (int k = lane; k < pieces; k += 32) {
+    const float2 ml = s.part_ml[prow(k)];
     sum = fmaf(exp2f(ml.x - mx), ml.y, sum);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   const float inv = 1.f / sum;
 #pragma unroll 4
-  for (int k = j; k < r.ranges; k += ways) {
-    const size_t pr = prow + k * pairs * 128;
+  for (int k = j; k < pieces; k += ways) {
+    const size_t pr = prow(k);
     const float f = exp2f(s.part_ml[pr].x - mx) * inv;
     const float4* src = reinterpret_cast<const float4*>(s.part_o + pr * kLat);
 #pragma unroll
@@ -1114,7 +1097,8 @@ __device__ __forceinline__ bool join_row(const AttnTreeArgs& a, const Scratch& s
 
 template <int kE>
 __global__ void __launch_bounds__(kE * 4)
-    tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s) {
+    tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
+                      int clusters) {
   constexpr int kThreads = kE * 4, kWarps = kE / 8, kSplit = 128 / kE;
   extern __shared__ __align__(16) uint8_t smem[];
   auto* so = reinterpret_cast<__nv_bfloat16*>(smem);
@@ -1139,7 +1123,7 @@ __global__ void __launch_bounds__(kE * 4)
     if (ways == 1) {
       for (int q = warp; q < kVTok; q += kWarps) {
         float4 acc[4] = {};
-        const bool ok = q < rows && join_row(a, s, n0 + q, h, 0, 1, lane, acc);
+        const bool ok = q < rows && join_row(s, clusters, n0 + q, h, 0, 1, lane, acc);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int at = q * kVLd + (c * 32 + lane) * 4;
@@ -1150,7 +1134,7 @@ __global__ void __launch_bounds__(kE * 4)
     } else {
       const int q = warp / ways, j = warp % ways;
       float4 acc[4] = {};
-      const bool ok = q < rows && join_row(a, s, n0 + q, h, j, ways, lane, acc);
+      const bool ok = q < rows && join_row(s, clusters, n0 + q, h, j, ways, lane, acc);
 #pragma unroll
       for (int c = 0; c < 4; ++c) part[warp * 128 + c * 32 + lane] = acc[c];
       if (j == 0 && lane == 0 && q < rows) live[q] = ok;
@@ -1198,13 +1182,14 @@ __global__ void __launch_bounds__(kE * 4)
 }
 
 template <int kE>
-cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int y, cudaStream_t stream) {
+cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int clusters, int y,
+                         cudaStream_t stream) {
   static ContextCache attr;
   auto kern = tree_value_kernel<kE>;
   const cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(kern), int(value_smem(kE)), &attr);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(kHeads * 128 / kE, unsigned(y)), kE * 4, value_smem(kE), stream>>>(a, s);
+  kern<<<dim3(kHeads * 128 / kE, unsigned(y)), kE * 4, value_smem(kE), stream>>>(a, s, clusters);
   return cudaGetLastError();
 }
 
@@ -1235,9 +1220,9 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   const int tiles = (a.N + kQTok - 1) / kQTok;
   const dim3 qgrid(kHeads * 4, unsigned(tiles < 3 ? tiles : 3) + 1);
   if (rotary)
-    tree_query_kernel<true><<<qgrid, kQThreads, 0, stream>>>(a, s, *rotary, clusters, err_word);
+    tree_query_kernel<true><<<qgrid, kQThreads, 0, stream>>>(a, s, *rotary, err_word);
   else
-    tree_query_kernel<false><<<qgrid, kQThreads, 0, stream>>>(a, s, RopeFreqs{}, clusters, err_word);
+    tree_query_kernel<false><<<qgrid, kQThreads, 0, stream>>>(a, s, RopeFreqs{}, err_word);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   float scale_log2 = a.scale * 1.4426950408889634f;
@@ -1250,8 +1235,8 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
       test_stall);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return a.N <= 2 * kVTok ? launch_value<64>(a, s, tiles, stream)
-                          : launch_value<128>(a, s, tiles < 2 ? tiles : 2, stream);
+  return a.N <= 2 * kVTok ? launch_value<64>(a, s, clusters, tiles, stream)
+                          : launch_value<128>(a, s, clusters, tiles < 2 ? tiles : 2, stream);
 }
 
 }  // namespace mla
