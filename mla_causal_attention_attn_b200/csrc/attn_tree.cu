@@ -364,65 +364,84 @@ static_assert(kASmem <= 225 * 1024, "shared memory budget");
 constexpr uint32_t kColO = 0, kColS = 256;       // tensor memory columns
 constexpr float kRescale = 8.f;                  // log2 growth of the maximum that rescales O
 
-// What a cluster visits: the items (pieces of pairs) of its share, tile by tile.
+// An item: a piece of a pair.
+struct Item {
+  TreeReq r;
+  int b, pair, t0, t1;
+  int cut_last;  // cut chunk of the last tile, or -1
+  int cut_row;   // its first row without a key
+};
+
+// The item that begins at position pos, of a share that ends at `end`.
+__device__ __noinline__ Item find_item(const TreeReq* req, int B, int page_shift, long long pos,
+                                       long long end) {
+  Item it;
+  int l = 0, h = B;  // the last request whose first position is at or before pos
+  while (h - l > 1) {
+    const int m = (l + h) >> 1;
+    if (req[m].base <= pos) l = m;
+    else h = m;
+  }
+  it.b = l;
+  it.r = req[l];
+  const long long rel = pos - it.r.base;
+  it.pair = int(rel / it.r.tiles);
+  it.t0 = int(rel - (long long)it.pair * it.r.tiles);
+  it.t1 = int(min((long long)it.r.tiles, it.t0 + (end - pos)));
+  // The chunk of 64 keys that the request's last key lies in has rows to be
+  // zeroed when a TMA box (min(page, 64) rows) goes past that key.
+  const int box = page_shift >= 6 ? 64 : 1 << page_shift;
+  it.cut_last = -1;
+  it.cut_row = it.r.keys & 63;
+  if (it.t1 == it.r.tiles && (it.r.keys & (box - 1)) != 0)
+    it.cut_last = ((it.r.keys - 1) & (kTileKeys - 1)) >> 6;
+  return it;
+}
+
+// A cluster's share: positions [x, y).
+__device__ __noinline__ longlong2 find_share(const long long* total_at, int cluster, int clusters) {
+  const long long total = *total_at;
+  clusters = shares(total, clusters);
+  if (cluster >= clusters) return make_longlong2(0, 0);
+  return make_longlong2(share_begin(total, cluster, clusters),
+                        share_begin(total, cluster + 1, clusters));
+}
+
+// What a cluster visits: the items of its share, tile by tile. Every role walks
+// for itself; the look-up is one function that they share.
 struct Walk {
   const AttnTreeArgs* a;
   const Scratch* s;
   long long pos, end;  // the next item's first position, the share's end
-  TreeReq r;
-  int b, pair, tile, t0, t1;
+  Item it;
+  int tile;
   int slot;      // of the item's partial result, or -1: the pair is whole
   int next_slot;
   int item_no;   // items begun so far - 1
-  int cut_last;  // cut chunk of the item's last tile, or -1
-  int cut_row;   // its first row without a key
 
   __device__ __forceinline__ Walk(const AttnTreeArgs& aa, const Scratch& ss, int cluster,
                                   int clusters)
-      : a(&aa), s(&ss), tile(0), t1(0), next_slot(2 * cluster), item_no(-1) {
-    const long long total = *ss.total;
-    clusters = shares(total, clusters);
-    pos = end = 0;
-    if (cluster < clusters) {
-      pos = share_begin(total, cluster, clusters);
-      end = share_begin(total, cluster + 1, clusters);
-    }
+      : a(&aa), s(&ss), tile(0), next_slot(2 * cluster), item_no(-1) {
+    const longlong2 share = find_share(ss.total, cluster, clusters);
+    pos = share.x;
+    end = share.y;
   }
   // Moves to the next tile; false at the end.
   __device__ __forceinline__ bool next() {
-    if (item_no >= 0 && ++tile < t1) return true;
+    if (item_no >= 0 && ++tile < it.t1) return true;
     if (pos >= end) return false;
-    int h = a->B;  // the last request whose first position is at or before pos
-    b = 0;
-    while (h - b > 1) {
-      const int m = (b + h) >> 1;
-      if (s->req[m].base <= pos) b = m;
-      else h = m;
-    }
-    r = s->req[b];
-    const long long rel = pos - r.base;
-    pair = int(rel / r.tiles);
-    t0 = int(rel - (long long)pair * r.tiles);
-    t1 = int(min((long long)r.tiles, t0 + (end - pos)));
-    tile = t0;
-    pos += t1 - t0;
-    slot = t0 == 0 && t1 == r.tiles ? -1 : next_slot;
+    it = find_item(s->req, a->B, a->page_shift, pos, end);
+    tile = it.t0;
+    pos += it.t1 - it.t0;
+    slot = it.t0 == 0 && it.t1 == it.r.tiles ? -1 : next_slot;
     next_slot |= 1;
     ++item_no;
-    // The chunk of 64 keys that the request's last key lies in has rows to be
-    // zeroed when a TMA box (min(page, 64) rows) goes past that key.
-    const int box = a->page_shift >= 6 ? 64 : 1 << a->page_shift;
-    cut_last = -1;
-    if (t1 == r.tiles && (r.keys & (box - 1)) != 0) {
-      cut_last = ((r.keys - 1) & (kTileKeys - 1)) >> 6;
-      cut_row = r.keys & 63;
-    }
     return true;
   }
-  __device__ __forceinline__ bool first() const { return tile == t0; }
-  __device__ __forceinline__ bool last() const { return tile + 1 == t1; }
+  __device__ __forceinline__ bool first() const { return tile == it.t0; }
+  __device__ __forceinline__ bool last() const { return tile + 1 == it.t1; }
   // The tile's chunk with rows to be zeroed, or -1.
-  __device__ __forceinline__ int cut() const { return last() ? cut_last : -1; }
+  __device__ __forceinline__ int cut() const { return last() ? it.cut_last : -1; }
 };
 
 // A position in a ring: slot and parity of its pass.
@@ -438,6 +457,9 @@ struct RingPos {
 };
 
 // The kernel's waits; a wait that does not succeed at once loops out of line.
+// They acquire at CTA scope, also where the other CTA's helper arrives: what
+// such a wait orders is read by the tensor core, behind tcgen05 fences, not by
+// the waiting thread (an acquire at cluster scope cost about 480 clocks each).
 struct Waits {
   int* abort_flag;
   unsigned int* err_word;
@@ -447,7 +469,7 @@ struct Waits {
 __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, const Waits w,
                                        uint32_t site) {
   const WaitCtl ctl{w.abort_flag, w.limit_ns, kErrKernelTree, w.err_word};
-  return mbar_wait_cluster_sleep(bar, parity, ctl, site);
+  return mbar_wait(bar, parity, ctl, site);
 }
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Waits& w,
@@ -580,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     const int per = 64 >> box_shift;  // boxes a 64-key chunk
     const int pmask = (1 << a.page_shift) - 1;
     auto page_at = [&](int key) -> int {  // page, or one past the last: zeros
-      const int id = key < walk.r.keys ? page_of(a, walk.b, key) : -1;
+      const int id = key < walk.it.r.keys ? page_of(a, walk.it.b, key) : -1;
       return id >= 0 ? id : a.num_pages;
     };
     uint32_t issued = 0;
@@ -594,9 +616,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         const int key = walk.tile * kTileKeys + int(rank) * 128 + (lane << box_shift);
         const int page = lane < 2 * per ? page_at(key) : 0;
         const bool first = walk.first();
-        const int node = 2 * walk.pair + int(rank);
+        const int node = 2 * walk.it.pair + int(rank);
         const int qrow =
-            node < walk.r.nodes ? (walk.r.start + node) * kHeads : a.N * kHeads;  // zeros
+            node < walk.it.r.nodes ? (walk.it.r.start + node) * kHeads : a.N * kHeads;  // zeros
 #pragma unroll 1
         for (int i = 0; ok && i < kKBlocks; ++i) {
           if (first) {
@@ -766,8 +788,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
           ok = wait_warp(&cut_full[m], (cuts >> 1) & 1u, waits, 13);
           if (!ok) break;
           uint8_t* blk = smem + kOffV + slot * kBlk;
-          for (int e = lane; e < (64 - walk.cut_row) * 16; e += 32) {  // 2 x 8 pieces of 16 bytes
-            const int row = walk.cut_row + (e >> 4);
+          for (int e = lane; e < (64 - walk.it.cut_row) * 16; e += 32) {  // 2 x 8 pieces of 16 bytes
+            const int row = walk.it.cut_row + (e >> 4);
             *reinterpret_cast<uint4*>(blk + ((e >> 3) & 1) * 8192 + row * 128 + (e & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           }
@@ -795,8 +817,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     const uint32_t hidden = scale_log2 < 0.f ? 0x7f800000u : 0xff800000u;
     bool ok = true;
     for (int g = 0; walk.next(); ++g) {
-      const int node = 2 * walk.pair + int(rank);
-      const bool live = node < walk.r.nodes;  // (the same for the whole CTA)
+      const int node = 2 * walk.it.pair + int(rank);
+      const bool live = node < walk.it.r.nodes;  // (the same for the whole CTA)
       if (walk.first()) {
         m = -INFINITY;
         l = 0.f;
@@ -804,8 +826,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       const int k0 = walk.tile * kTileKeys + half * 128;  // this thread's 128 keys
       const int n_pg = 128 >> a.page_shift;               // pages in the range, 1 .. 8
       bool has = false;
-      if (lane < n_pg && k0 + (lane << a.page_shift) < walk.r.keys)
-        has = page_of(a, walk.b, k0 + (lane << a.page_shift)) >= 0;
+      if (lane < n_pg && k0 + (lane << a.page_shift) < walk.it.r.keys)
+        has = page_of(a, walk.it.b, k0 + (lane << a.page_shift)) >= 0;
       const uint32_t pages = __ballot_sync(0xffffffffu, has);
       // After a wait that gave up (ok false) a warp goes on without waiting, so
       // that it meets the others at the named barriers, until all leave together.
@@ -815,13 +837,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       const uint32_t sc = lanes + kColS + 128u * uint32_t(g & 1);
       float mt = -INFINITY;
       if (live) {
-        if (k0 + 128 > walk.r.ctx || pages != (1u << n_pg) - 1u) {
+        if (k0 + 128 > walk.it.r.ctx || pages != (1u << n_pg) - 1u) {
           // hide what the node does not see
           const uint32_t* mask =
-              a.tree_mask ? a.tree_mask + size_t(walk.r.start + node) * a.mask_words : nullptr;
+              a.tree_mask ? a.tree_mask + size_t(walk.it.r.start + node) * a.mask_words : nullptr;
 #pragma unroll 1
           for (int w = 0; w < 4; ++w) {
-            uint32_t see = seen_keys(a, walk.r, mask, node, k0 + 32 * w);
+            uint32_t see = seen_keys(a, walk.it.r, mask, node, k0 + 32 * w);
             if (a.page_shift == 4) {
               if (!((pages >> (2 * w)) & 1u)) see &= 0xffff0000u;
               if (!((pages >> (2 * w + 1)) & 1u)) see &= 0x0000ffffu;
@@ -861,35 +883,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         m = mt;
       }
       const float mx = m == -INFINITY ? 0.f : m;
-      uint32_t pk[64];
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      if (live) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t r[32];
-          tmem_ld32(sc + 32 * w, r);
-          tmem_ld_wait();
-          reg_fence(r);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            ffma2(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scale_log2,
-                  scale_log2, -mx, -mx);
-            x0 = fast_exp2(x0);
-            x1 = fast_exp2(x1);
-            fadd2(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], acc[2 * (i & 1)], acc[2 * (i & 1) + 1],
-                  x0, x1);
-            pk[16 * w + i] = pack_bf16x2(x0, x1);
-          }
-        }
-      } else {  // a pair's absent second node
-#pragma unroll
-        for (int i = 0; i < 64; ++i) pk[i] = 0u;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[g & 1]);
-      l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
       // O holds the products up to tile g - 1: rescale it once they are done.
       // Its halves of columns belong to different threads, all of one alpha
       // per row; alpha is 1 in an item's first tile.
@@ -913,16 +906,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       // warps of the second half report their part of it before their own P.
       __syncwarp();
       if (ok && half == 1 && lane == 0) mbar_arrive(&p_full[0]);
-      // P into shared memory once the value products have read the last tile's
+      // P goes to shared memory once the value products have read the last
+      // tile's: for the first half of the keys in the middle of those products,
+      // for the second half at their end, half of a tile's products before they
+      // are needed.
       if (ok && g > 0) ok = wait_warp(&p_free[half], uint32_t(g - 1) & 1u, waits, 22);
       uint8_t* pr = smem + kOffP + half * 2 * kQBlk + row * 128;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int w = 0; w < 4; ++w) {
+        uint32_t r[32];
+        tmem_ld32(sc + 32 * w, r);
+        tmem_ld_wait();
+        reg_fence(r);
+        uint32_t pk[16];
 #pragma unroll
-      for (int u = 0; u < 16; ++u)
-        *reinterpret_cast<uint4*>(pr + (u >> 3) * kQBlk + (((u & 7) ^ (row & 7)) << 4)) =
-            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+        for (int i = 0; i < 16; ++i) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scale_log2,
+                scale_log2, -mx, -mx);
+          x0 = fast_exp2(x0);
+          x1 = fast_exp2(x1);
+          fadd2(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], acc[2 * (i & 1)], acc[2 * (i & 1) + 1], x0,
+                x1);
+          pk[i] = live ? pack_bf16x2(x0, x1) : 0u;  // (P = 0 for a pair's absent second node)
+        }
+        uint8_t* pw = pr + (w >> 1) * kQBlk;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<uint4*>(pw + (((4 * (w & 1) + u) ^ (row & 7)) << 4)) =
+              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+      }
+      l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+      tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&p_full[half]);
+      if (ok && lane == 0) {
+        mbar_arrive(&s_free[g & 1]);
+        mbar_arrive(&p_full[half]);
+      }
       if (!walk.last()) continue;
 
       // ---- epilogue of the item
@@ -939,21 +961,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         dst = s.part_o + prow * kLat;
       } else {
         f = lsum > 0.f ? 1.f / lsum : 0.f;
-        dst = s.o + (size_t(walk.r.start + node) * kHeads + row) * kLat;
+        dst = s.o + (size_t(walk.it.r.start + node) * kHeads + row) * kLat;
       }
+      // Row by row through shared memory (P's, free until the next tile's), so
+      // that a store instruction writes four whole 128-byte lines: a thread
+      // writing its own row took 10 thousand clocks an item.
+      float* base = dst - size_t(row) * kLat;
+      uint8_t* mine = smem + kOffP + (warp & 3) * 4096;  // [32 rows][128 bytes]
+      const int row0 = row & 32;                         // the warp's first row
 #pragma unroll 1
-      for (int c = 0; ok && c < 8; ++c) {
+      for (int c = 0; ok && live && c < 8; ++c) {
         uint32_t r[32];
         tmem_ld32(lanes + kColO + 32 * c, r);
         tmem_ld_wait();
         reg_fence(r);
-        if (live) {
-          float4* d = reinterpret_cast<float4*>(dst + (c >> 2) * 256 + half * 128 + (c & 3) * 32);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            d[i] = make_float4(__uint_as_float(r[4 * i]) * f, __uint_as_float(r[4 * i + 1]) * f,
-                               __uint_as_float(r[4 * i + 2]) * f, __uint_as_float(r[4 * i + 3]) * f);
+        for (int u = 0; u < 8; ++u)
+          *reinterpret_cast<float4*>(mine + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+              make_float4(__uint_as_float(r[4 * u]) * f, __uint_as_float(r[4 * u + 1]) * f,
+                          __uint_as_float(r[4 * u + 2]) * f, __uint_as_float(r[4 * u + 3]) * f);
+        __syncwarp();
+        float* to = base + (c >> 2) * 256 + half * 128 + (c & 3) * 32 + (lane & 7) * 4;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = 4 * k + (lane >> 3);
+          *reinterpret_cast<float4*>(to + size_t(row0 + rr) * kLat) =
+              *reinterpret_cast<const float4*>(mine + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
         }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -965,7 +1000,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   __syncwarp();
   tc_fence_before();
   cluster_sync();
-  if (warp == 9 && lane == 0 && n_cut[1] < n_cut[0]) {
+  // Without an abort every block that was issued has been read by a product.
+  const bool aborted =
+      abort_flag != 0 || ld_shared_cluster_u32(mapa_shared(smem_u32(&abort_flag), rank ^ 1)) != 0;
+  if (aborted && warp == 9 && lane == 0 && n_cut[1] < n_cut[0]) {
     // cut blocks that were issued but not reported (after an abort): they land
     // on this CTA's barriers, then count on the even CTA's
     int zero = 0;
@@ -983,8 +1021,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     }
   }
   __syncwarp();
-  cluster_sync();
-  if (leader && warp == 0 && lane == 0) {
+  if (aborted) cluster_sync();
+  if (aborted && leader && warp == 0 && lane == 0) {
     // Account for blocks that only one CTA issued (possible only after an
     // abort), then wait for the last phase of every slot.
     int zero = 0;
