@@ -55,6 +55,7 @@ struct Scratch {
   long long* total;    // W
   TreeReq* req;        // [B]
   int* row_req;        // [N]: the last request that starts at or before the row
+  int4* row_info;      // [N]: where the row's results are (RowInfo)
   __nv_bfloat16* q;    // [N, 64, 576]
   float* o;            // [N, 64, 512], pairs in one share
   float* part_o;       // [kMaxSlots][128][512]
@@ -72,6 +73,8 @@ Scratch carve(void* base, int B, int64_t N) {
   p += up256(size_t(B) * sizeof(TreeReq));
   s.row_req = reinterpret_cast<int*>(p);
   p += up256(size_t(N) * 4);
+  s.row_info = reinterpret_cast<int4*>(p);
+  p += up256(size_t(N) * 16);
   s.q = reinterpret_cast<__nv_bfloat16*>(p);
   p += up256(size_t(N) * kHeads * kRow * 2);
   s.o = reinterpret_cast<float*>(p);
@@ -190,7 +193,7 @@ __device__ __forceinline__ void cp_wait() {
 // q~ = U_h^T q_nope: 16 tokens x 128 latent columns a step, contraction over
 // the head's 128 key dims. Grid (64 heads * 4 column quarters, y + 1): a CTA
 // keeps its 32 KB of weights in shared memory and walks every y-th token tile,
-// the next one on its way. The CTAs of the last y row do the rest: the first
+// the next ones on their way. The CTAs of the first y row do the rest: the first
 // lays out the schedule and clears the status word, the others rotate the
 // rotary parts (a warp turns 8 heads of a token by one sine and cosine per
 // lane) and find the rows' requests.
@@ -245,7 +248,7 @@ template <bool kRope>
 __global__ void __launch_bounds__(kQThreads)
     tree_query_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
                       const __grid_constant__ RopeFreqs f, unsigned int* err_word) {
-  if (blockIdx.y == gridDim.y - 1) {
+  if (blockIdx.y == 0) {
     if (blockIdx.x == 0) {
       if (threadIdx.x == 0) *err_word = 0u;
       schedule(a, s);
@@ -254,35 +257,36 @@ __global__ void __launch_bounds__(kQThreads)
     }
     return;
   }
-  __shared__ __align__(16) __nv_bfloat16 sq[2][kQTok * kQLd];
+  __shared__ __align__(16) __nv_bfloat16 sq[3][kQTok * kQLd];
   __shared__ __align__(16) __nv_bfloat16 sw[kNope * kQLd];
   const int h = blockIdx.x >> 2, c0 = (blockIdx.x & 3) * kQCols;
   const int tiles = (a.N + kQTok - 1) / kQTok, step = gridDim.y - 1;
   const auto* qn = static_cast<const __nv_bfloat16*>(a.q_nope);
   const auto* w = static_cast<const __nv_bfloat16*>(a.w_kv_b) + size_t(h) * 256 * kLat + c0;
   static_assert(kQTok * (kNope / 8) == kQThreads, "one piece of a query tile per thread");
-  auto load = [&](int tile, int buf) {
+  auto load = [&](int tile, int buf) {  // (a group of its own, empty past the last tile)
     const int n = threadIdx.x / (kNope / 8), c = threadIdx.x % (kNope / 8) * 8;
     const int row = min(tile * kQTok + n, a.N - 1);
-    cp16(smem_u32(&sq[buf][n * kQLd + c]), qn + (size_t(row) * kHeads + h) * kNope + c, true);
+    if (tile < tiles)
+      cp16(smem_u32(&sq[buf][n * kQLd + c]), qn + (size_t(row) * kHeads + h) * kNope + c, true);
     cp_commit();
   };
   for (int i = threadIdx.x; i < kNope * (kQCols / 8); i += kQThreads) {
     const int e = i / (kQCols / 8), c = i % (kQCols / 8) * 8;
     cp16(smem_u32(sw + e * kQLd + c), w + size_t(e) * kLat + c, true);
   }
-  load(blockIdx.y, 0);
+  cp_commit();
+  const int first = blockIdx.y - 1;
+  load(first, 0);
+  load(first + step, 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cw = warp * 16;  // this warp's 16 columns: two n-tiles
   const int g = lane >> 2, t = lane & 3;
   int buf = 0;
-  for (int tile = blockIdx.y; tile < tiles; tile += step, buf ^= 1) {
-    if (tile + step < tiles) {
-      load(tile + step, buf ^ 1);
-      cp_wait<1>();
-    } else {
-      cp_wait<0>();
-    }
+  for (int tile = first; tile < tiles; tile += step, buf = buf == 2 ? 0 : buf + 1) {
+    // two tiles ahead, into the buffer the tile before this one left
+    load(tile + 2 * step, buf == 0 ? 2 : buf - 1);
+    cp_wait<2>();
     __syncthreads();
     float d[2][4] = {};
 #pragma unroll
@@ -293,16 +297,20 @@ __global__ void __launch_bounds__(kQThreads)
       mma_16816(d[0], fa, fb[0], fb[1]);
       mma_16816(d[1], fa, fb[2], fb[3]);
     }
+    // through the query tile's own buffer, so that a row leaves in whole lines
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int n = tile * kQTok + g + 8 * half;
-        if (n < a.N)
-          *reinterpret_cast<uint32_t*>(s.q + (size_t(n) * kHeads + h) * kRow + c0 + cw + 8 * j +
-                                       2 * t) = pack_bf16x2(d[j][2 * half], d[j][2 * half + 1]);
-      }
-    __syncthreads();  // the buffer is loaded again two tiles later
+      for (int half = 0; half < 2; ++half)
+        *reinterpret_cast<uint32_t*>(&sq[buf][(g + 8 * half) * kQLd + cw + 8 * j + 2 * t]) =
+            pack_bf16x2(d[j][2 * half], d[j][2 * half + 1]);
+    __syncthreads();
+    const int n = tile * kQTok + threadIdx.x / 16, c = threadIdx.x % 16 * 8;
+    if (n < a.N)
+      *reinterpret_cast<uint4*>(s.q + (size_t(n) * kHeads + h) * kRow + c0 + c) =
+          *reinterpret_cast<const uint4*>(&sq[buf][(threadIdx.x / 16) * kQLd + c]);
+    __syncthreads();  // the buffer is loaded again
   }
 }
 
@@ -405,6 +413,24 @@ __device__ __noinline__ longlong2 find_share(const long long* total_at, int clus
   if (cluster >= clusters) return make_longlong2(0, 0);
   return make_longlong2(share_begin(total, cluster, clusters),
                         share_begin(total, cluster + 1, clusters));
+}
+
+// Where row n's latent results are: x pieces (0: the row belongs to no request,
+// 1: whole, in Scratch::o, -1: a request without keys), y the slot of the first
+// piece, z the first piece's cluster.
+__device__ __noinline__ int4 place_of(const Scratch& s, int clusters, int n) {
+  const TreeReq r = s.req[s.row_req[n]];
+  const int node = n - r.start;
+  if (node < 0 || node >= r.nodes) return make_int4(0, 0, 0, 0);
+  if (r.tiles == 0) return make_int4(-1, 0, 0, 0);
+  const long long total = *s.total;
+  clusters = shares(total, clusters);
+  const long long p0 = r.base + (long long)(node >> 1) * r.tiles;
+  const int c0 = share_of(total, p0, clusters);
+  const int pieces = share_of(total, p0 + r.tiles - 1, clusters) - c0 + 1;
+  const int first = 2 * c0 + (share_begin(total, c0, clusters) < p0 ? 1 : 0);
+  // a partial result's rows 64 .. 127 are the pair's second node
+  return make_int4(pieces, first * 128 + (node & 1) * 64, c0, node & 1);
 }
 
 // What a cluster visits: the items of its share, tile by tile. Every role walks
@@ -762,7 +788,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ helper (odd CTA): P
-    if (lane == 0 && !leader) {
+    // (even CTA: the rows' places for the value kernel)
+    if (leader) {
+      for (int n = int(blockIdx.x >> 1) * 32 + lane; n < a.N; n += int(gridDim.x >> 1) * 32)
+        s.row_info[n] = place_of(s, int(gridDim.x >> 1), n);
+    } else if (lane == 0) {
       bool ok = true;
       for (int g = 0; ok && walk.next(); ++g)
 #pragma unroll 1
@@ -1058,9 +1088,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
 // ---------------------------------------------------------------- value
 // out[n, h * 128 + e] = sum_r o~[n, h, r] V_h[e, r]: 16 tokens x kE value dims
 // a step. Grid (64 heads * 128 / kE, y): a CTA keeps its weights in shared
-// memory and walks every y-th token tile. The rows of o~ are joined from the
-// partial results of their request first, by one warp a row or, when there are
-// fewer rows than warps, by several that share the ranges.
+// memory and walks every y-th token tile; while a tile's product runs, the next
+// one's rows are on their way to registers (up to two pieces a row). The rows
+// of o~ are joined from their pieces first, by one warp a row or, when there
+// are fewer rows than warps, by several that share the pieces.
 constexpr int kVTok = 16;
 constexpr int kVLd = kLat + 8;
 constexpr size_t value_smem(int e) {
@@ -1077,67 +1108,90 @@ __device__ __forceinline__ void split_store(__nv_bfloat16* hi, __nv_bfloat16* lo
                  pack_bf16x2(x.z - __uint_as_float(h1 << 16), x.w - __uint_as_float(h1 & 0xffff0000u)));
 }
 
-// Row n's latent result of head h: its columns 4 (32 c + lane) .. + 3 for c =
-// 0..3, over the pieces j, j + ways, ... of its pair; false for a row of no
-// request.
-__device__ __forceinline__ bool join_row(const Scratch& s, int clusters, int n, int h, int j,
-                                         int ways, int lane, float4 (&acc)[4]) {
-  const TreeReq r = s.req[s.row_req[n]];
-  const int node = n - r.start;
-  if (node < 0 || node >= r.nodes) return false;
-  if (r.tiles == 0) return true;
-  const long long total = *s.total;
-  clusters = shares(total, clusters);
-  const long long p0 = r.base + (long long)(node >> 1) * r.tiles;
-  const int c0 = share_of(total, p0, clusters);
-  const int pieces = share_of(total, p0 + r.tiles - 1, clusters) - c0 + 1;
+__device__ __forceinline__ float4 axpy4(float f, float4 x, float4 y) {
+  return make_float4(fmaf(f, x.x, y.x), fmaf(f, x.y, y.y), fmaf(f, x.z, y.z), fmaf(f, x.w, y.w));
+}
+
+// A row of one head: its place, and what is already in registers (a lane has
+// columns 4 (32 c + lane) .. + 3 for c = 0..3).
+struct Row {
+  int4 at;         // RowInfo
+  float2 ml0, ml1;
+  float4 v0[4], v1[4];
+};
+
+// Starts the loads of row n, head h (one or two pieces).
+__device__ __forceinline__ void fetch_row(const Scratch& s, int n, int h, int lane, Row& r) {
+  const float* p0 = nullptr;
+  if (r.at.x == 1) {
+    p0 = s.o + (size_t(n) * kHeads + h) * kLat;
+  } else if (r.at.x == 2) {
+    const size_t a0 = size_t(r.at.y) + h;
+    const size_t a1 = size_t(2 * (r.at.z + 1)) * 128 + r.at.w * 64 + h;
+    r.ml0 = s.part_ml[a0];
+    r.ml1 = s.part_ml[a1];
+    p0 = s.part_o + a0 * kLat;
+    const float4* p1 = reinterpret_cast<const float4*>(s.part_o + a1 * kLat);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r.v1[c] = p1[c * 32 + lane];
+  }
+  if (p0)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r.v0[c] = reinterpret_cast<const float4*>(p0)[c * 32 + lane];
+}
+
+// The row's latent result, of the pieces j, j + ways, ... only.
+__device__ __forceinline__ void join_row(const Scratch& s, int h, int j, int ways, int lane,
+                                         const Row& r, float4 (&acc)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int pieces = r.at.x;
+  if (pieces <= 0 || (pieces <= 2 && j > 0)) return;
   if (pieces == 1) {
-    const float4* src = reinterpret_cast<const float4*>(s.o + (size_t(n) * kHeads + h) * kLat);
-    if (j == 0)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = src[c * 32 + lane];
-    return true;
-  }
-  // row of piece k's partial result
-  const int first = 2 * c0 + (share_begin(total, c0, clusters) < p0 ? 1 : 0);
-  auto prow = [&](int k) {
-    return size_t(k == 0 ? first : 2 * (c0 + k)) * 128 + (node & 1) * 64 + h;
-  };
-  float mx = -INFINITY;
-  for (int k = lane; k < pieces; k += 32) mx = fmaxf(mx, s.part_ml[prow(k)].x);
+    for (int c = 0; c < 4; ++c) acc[c] = r.v0[c];
+  } else if (pieces == 2) {
+    const float mx = fmaxf(r.ml0.x, r.ml1.x);
+    if (mx == -INFINITY) return;  // nothing visible: zeros
+    float f0 = exp2f(r.ml0.x - mx), f1 = exp2f(r.ml1.x - mx);
+    const float inv = 1.f / fmaf(f0, r.ml0.y, f1 * r.ml1.y);
+    f0 *= inv;
+    f1 *= inv;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  if (mx == -INFINITY) return true;  // nothing visible: zeros
-  float sum = 0.f;
-  for (int k = lane; k < pieces; k += 32) {
-    const float2 ml = s.part_ml[prow(k)];
-    sum = fmaf(exp2f(ml.x - mx), ml.y, sum);
-  }
+    for (int c = 0; c < 4; ++c) acc[c] = axpy4(f0, r.v0[c], axpy4(f1, r.v1[c], acc[c]));
+  } else {
+    auto prow = [&](int k) {
+      return size_t(k == 0 ? r.at.y : 2 * (r.at.z + k) * 128 + r.at.w * 64) + h;
+    };
+    float mx = -INFINITY;
+    for (int k = lane; k < pieces; k += 32) mx = fmaxf(mx, s.part_ml[prow(k)].x);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  const float inv = 1.f / sum;
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    if (mx == -INFINITY) return;
+    float sum = 0.f;
+    for (int k = lane; k < pieces; k += 32) {
+      const float2 ml = s.part_ml[prow(k)];
+      sum = fmaf(exp2f(ml.x - mx), ml.y, sum);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float inv = 1.f / sum;
 #pragma unroll 4
-  for (int k = j; k < pieces; k += ways) {
-    const size_t pr = prow(k);
-    const float f = exp2f(s.part_ml[pr].x - mx) * inv;
-    const float4* src = reinterpret_cast<const float4*>(s.part_o + pr * kLat);
+    for (int k = j; k < pieces; k += ways) {
+      const size_t pr = prow(k);
+      const float f = exp2f(s.part_ml[pr].x - mx) * inv;
+      const float4* src = reinterpret_cast<const float4*>(s.part_o + pr * kLat);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 v = src[c * 32 + lane];
-      acc[c].x = fmaf(f, v.x, acc[c].x);
-      acc[c].y = fmaf(f, v.y, acc[c].y);
-      acc[c].z = fmaf(f, v.z, acc[c].z);
-      acc[c].w = fmaf(f, v.w, acc[c].w);
+      for (int c = 0; c < 4; ++c) acc[c] = axpy4(f, src[c * 32 + lane], acc[c]);
     }
   }
-  return true;
 }
 
 template <int kE>
 __global__ void __launch_bounds__(kE * 4)
-    tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
-                      int clusters) {
+    tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s) {
   constexpr int kThreads = kE * 4, kWarps = kE / 8, kSplit = 128 / kE;
+  constexpr int kRows = kVTok / kWarps;  // a warp's rows of a full tile
   extern __shared__ __align__(16) uint8_t smem[];
   auto* so = reinterpret_cast<__nv_bfloat16*>(smem);
   auto* sl = so + kVTok * kVLd;
@@ -1153,44 +1207,71 @@ __global__ void __launch_bounds__(kE * 4)
     cp16(smem_u32(sw + e * kVLd + c), w + size_t(e) * kLat + c, true);
   }
   cp_commit();
-  const int tiles = (a.N + kVTok - 1) / kVTok;
-  for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+  const int tiles = (a.N + kVTok - 1) / kVTok, step = gridDim.y;
+  // rows q = warp, warp + kWarps, .. of a tile; a tile of few rows: several
+  // warps a row
+  Row rows[kRows];
+  auto ways_of = [&](int tile) { return max(kWarps / min(kVTok, a.N - tile * kVTok), 1); };
+  auto row_of = [&](int tile, int k) {
+    const int ways = ways_of(tile);
+    const int n = tile * kVTok + (ways > 1 ? (k == 0 ? warp / ways : kVTok) : warp + k * kWarps);
+    return n < min((tile + 1) * kVTok, a.N) ? n : -1;
+  };
+  auto place = [&](int tile) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int n = tile < tiles ? row_of(tile, k) : -1;
+      rows[k].at = n >= 0 ? s.row_info[n] : make_int4(0, 0, 0, 0);
+    }
+  };
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (tile < tiles && rows[k].at.x > 0) fetch_row(s, row_of(tile, k), h, lane, rows[k]);
+  };
+  place(blockIdx.y);
+  fetch(blockIdx.y);
+  for (int tile = blockIdx.y; tile < tiles; tile += step) {
     const int n0 = tile * kVTok;
-    const int rows = min(kVTok, a.N - n0);
-    const int ways = max(kWarps / rows, 1);
+    const int ways = ways_of(tile);
     if (ways == 1) {
-      for (int q = warp; q < kVTok; q += kWarps) {
-        float4 acc[4] = {};
-        const bool ok = q < rows && join_row(s, clusters, n0 + q, h, 0, 1, lane, acc);
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int q = warp + k * kWarps;
+        float4 acc[4];
+        join_row(s, h, 0, 1, lane, rows[k], acc);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int at = q * kVLd + (c * 32 + lane) * 4;
           split_store(so + at, sl + at, acc[c]);
         }
-        if (lane == 0) live[q] = ok;
+        if (lane == 0) live[q] = rows[k].at.x != 0;
       }
     } else {
+      const int n_rows = a.N - n0;
       const int q = warp / ways, j = warp % ways;
-      float4 acc[4] = {};
-      const bool ok = q < rows && join_row(s, clusters, n0 + q, h, j, ways, lane, acc);
+      float4 acc[4];
+      join_row(s, h, j, ways, lane, rows[0], acc);
 #pragma unroll
       for (int c = 0; c < 4; ++c) part[warp * 128 + c * 32 + lane] = acc[c];
-      if (j == 0 && lane == 0 && q < rows) live[q] = ok;
+      if (j == 0 && lane == 0 && q < n_rows) live[q] = rows[0].at.x != 0;
       __syncthreads();
       for (int i = tid; i < kVTok * 128; i += kThreads) {
         const int qq = i >> 7, c = i & 127;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (qq < rows)
+        if (qq < n_rows)
           for (int k = 0; k < ways; ++k) {
             const float4 y = part[(qq * ways + k) * 128 + c];
             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
           }
         split_store(so + qq * kVLd + c * 4, sl + qq * kVLd + c * 4, x);
-        if (c == 0 && qq >= rows) live[qq] = 0;
+        if (c == 0 && qq >= n_rows) live[qq] = 0;
       }
     }
+    place(tile + step);
     cp_wait<0>();
     __syncthreads();
+    fetch(tile + step);
     float d[4] = {};
 #pragma unroll 4
     for (int k = 0; k < kLat / 16; k += 2) {
@@ -1220,21 +1301,20 @@ __global__ void __launch_bounds__(kE * 4)
 }
 
 template <int kE>
-cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int clusters, int y,
-                         cudaStream_t stream) {
+cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int y, cudaStream_t stream) {
   static ContextCache attr;
   auto kern = tree_value_kernel<kE>;
   const cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(kern), int(value_smem(kE)), &attr);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(kHeads * 128 / kE, unsigned(y)), kE * 4, value_smem(kE), stream>>>(a, s, clusters);
+  kern<<<dim3(kHeads * 128 / kE, unsigned(y)), kE * 4, value_smem(kE), stream>>>(a, s);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t attn_tree_scratch_bytes(int B, int64_t N) {
-  return 256 + up256(size_t(B) * sizeof(TreeReq)) + up256(size_t(N) * 4) + up256(size_t(N) * kHeads * kRow * 2) +
+  return 256 + up256(size_t(B) * sizeof(TreeReq)) + up256(size_t(N) * 4) + up256(size_t(N) * 16) + up256(size_t(N) * kHeads * kRow * 2) +
          up256(size_t(N) * kHeads * kLat * 4) + up256(size_t(kMaxSlots) * 128 * sizeof(float2)) +
          size_t(kMaxSlots) * 128 * kLat * 4;
 }
@@ -1273,8 +1353,8 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
       test_stall);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return a.N <= 2 * kVTok ? launch_value<64>(a, s, clusters, tiles, stream)
-                          : launch_value<128>(a, s, clusters, tiles < 2 ? tiles : 2, stream);
+  return a.N <= 2 * kVTok ? launch_value<64>(a, s, tiles, stream)
+                          : launch_value<128>(a, s, tiles < 2 ? tiles : 2, stream);
 }
 
 }  // namespace mla
