@@ -1087,15 +1087,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
 
 // ---------------------------------------------------------------- value
 // out[n, h * 128 + e] = sum_r o~[n, h, r] V_h[e, r]: 16 tokens x kE value dims
-// a step. Grid (64 heads * 128 / kE, y): a CTA keeps its weights in shared
-// memory and walks every y-th token tile; while a tile's product runs, the next
-// one's rows are on their way to registers (up to two pieces a row). The rows
-// of o~ are joined from their pieces first, by one warp a row or, when there
-// are fewer rows than warps, by several that share the pieces.
+// a step. Grid (64 heads * 128 / kE, y): a CTA walks every y-th token tile with
+// its weights in registers, a warp 64 dims x 64 latent columns of them, so that
+// shared memory carries only the rows (with the weights read from it every tile
+// it took 5 us a tile) and the eight warps' sums. The rows of o~ are joined
+// from their pieces first, by one warp a row or, when there are fewer rows than
+// warps, by several that share the pieces; the next tile's rows (of one or two
+// pieces) are copied to shared memory meanwhile.
 constexpr int kVTok = 16;
 constexpr int kVLd = kLat + 8;
-constexpr size_t value_smem(int e) {
-  return size_t(2 * kVTok + e) * kVLd * 2 + size_t(e / 8) * kLat * 4;
+constexpr int kVGroups = 8;  // warps that share 64 dims, 64 latent columns each
+constexpr uint32_t kVRows = 2 * kVTok * kVLd * 2;        // a tile's rows, high and low parts
+constexpr uint32_t kVRaw = 2 * kVTok * kLat * 4;         // the next tile's pieces
+constexpr uint32_t value_red(int e) { return kVGroups * kVTok * (e + 4) * 4; }
+constexpr uint32_t value_smem(int e) {
+  // rows, then the weights at first, the pieces and sums (or the shares of a
+  // row) after that
+  const uint32_t w = e * kVLd * 2, later = kVRaw + value_red(e);
+  return 2 * kVRows + (w > later ? w : later);
 }
 
 // x as a bf16 and the bf16 of what it leaves: together 2^-17 of x, so that the
@@ -1112,92 +1121,82 @@ __device__ __forceinline__ float4 axpy4(float f, float4 x, float4 y) {
   return make_float4(fmaf(f, x.x, y.x), fmaf(f, x.y, y.y), fmaf(f, x.z, y.z), fmaf(f, x.w, y.w));
 }
 
-// A row of one head: its place, and what is already in registers (a lane has
-// columns 4 (32 c + lane) .. + 3 for c = 0..3).
-struct Row {
-  int4 at;         // RowInfo
-  float2 ml0, ml1;
-  float4 v0[4], v1[4];
-};
-
-// Starts the loads of row n, head h (one or two pieces).
-__device__ __forceinline__ void fetch_row(const Scratch& s, int n, int h, int lane, Row& r) {
-  const float* p0 = nullptr;
-  if (r.at.x == 1) {
-    p0 = s.o + (size_t(n) * kHeads + h) * kLat;
-  } else if (r.at.x == 2) {
-    const size_t a0 = size_t(r.at.y) + h;
-    const size_t a1 = size_t(2 * (r.at.z + 1)) * 128 + r.at.w * 64 + h;
-    r.ml0 = s.part_ml[a0];
-    r.ml1 = s.part_ml[a1];
-    p0 = s.part_o + a0 * kLat;
-    const float4* p1 = reinterpret_cast<const float4*>(s.part_o + a1 * kLat);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) r.v1[c] = p1[c * 32 + lane];
-  }
-  if (p0)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) r.v0[c] = reinterpret_cast<const float4*>(p0)[c * 32 + lane];
+// First partial row of piece k of a row of head h.
+__device__ __forceinline__ size_t piece_row(int4 at, int k, int h) {
+  return size_t(k == 0 ? at.y : 2 * (at.z + k) * 128 + at.w * 64) + h;
 }
 
-// The row's latent result, of the pieces j, j + ways, ... only.
-__device__ __forceinline__ void join_row(const Scratch& s, int h, int j, int ways, int lane,
-                                         const Row& r, float4 (&acc)[4]) {
+// A row of one head: its place, and the maxima and sums of its first two pieces.
+struct RowPlace {
+  int4 at;
+  float2 ml0, ml1;
+};
+
+// The latent result of row n, head h, columns 4 (32 c + lane) .. + 3 for c =
+// 0..3, of the pieces j, j + ways, ... only; raw: its first two pieces in
+// shared memory.
+__device__ __forceinline__ void join_row(const Scratch& s, const RowPlace& r, int h, int j, int ways,
+                                         int lane, const float4* raw, float4 (&acc)[4]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int pieces = r.at.x;
-  if (pieces <= 0 || (pieces <= 2 && j > 0)) return;
-  if (pieces == 1) {
+  if (pieces <= 0) return;
+  if (pieces <= 2) {
+    if (j > 0) return;
+    float f0 = 1.f, f1 = 0.f;
+    if (pieces == 2) {
+      const float mx = fmaxf(r.ml0.x, r.ml1.x);
+      if (mx == -INFINITY) return;  // nothing visible: zeros
+      f0 = exp2f(r.ml0.x - mx);
+      f1 = exp2f(r.ml1.x - mx);
+      const float inv = 1.f / fmaf(f0, r.ml0.y, f1 * r.ml1.y);
+      f0 *= inv;
+      f1 *= inv;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = r.v0[c];
-  } else if (pieces == 2) {
-    const float mx = fmaxf(r.ml0.x, r.ml1.x);
-    if (mx == -INFINITY) return;  // nothing visible: zeros
-    float f0 = exp2f(r.ml0.x - mx), f1 = exp2f(r.ml1.x - mx);
-    const float inv = 1.f / fmaf(f0, r.ml0.y, f1 * r.ml1.y);
-    f0 *= inv;
-    f1 *= inv;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = axpy4(f0, r.v0[c], axpy4(f1, r.v1[c], acc[c]));
-  } else {
-    auto prow = [&](int k) {
-      return size_t(k == 0 ? r.at.y : 2 * (r.at.z + k) * 128 + r.at.w * 64) + h;
-    };
-    float mx = -INFINITY;
-    for (int k = lane; k < pieces; k += 32) mx = fmaxf(mx, s.part_ml[prow(k)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    if (mx == -INFINITY) return;
-    float sum = 0.f;
-    for (int k = lane; k < pieces; k += 32) {
-      const float2 ml = s.part_ml[prow(k)];
-      sum = fmaf(exp2f(ml.x - mx), ml.y, sum);
+      for (int c = 0; c < 4; ++c) acc[c] = axpy4(f1, raw[kVTok * kLat / 4 + c * 32 + lane], acc[c]);
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const float inv = 1.f / sum;
+    for (int c = 0; c < 4; ++c) acc[c] = axpy4(f0, raw[c * 32 + lane], acc[c]);
+    return;
+  }
+  float mx = -INFINITY;
+  for (int k = lane; k < pieces; k += 32) mx = fmaxf(mx, s.part_ml[piece_row(r.at, k, h)].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  if (mx == -INFINITY) return;
+  float sum = 0.f;
+  for (int k = lane; k < pieces; k += 32) {
+    const float2 ml = s.part_ml[piece_row(r.at, k, h)];
+    sum = fmaf(exp2f(ml.x - mx), ml.y, sum);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const float inv = 1.f / sum;
 #pragma unroll 4
-    for (int k = j; k < pieces; k += ways) {
-      const size_t pr = prow(k);
-      const float f = exp2f(s.part_ml[pr].x - mx) * inv;
-      const float4* src = reinterpret_cast<const float4*>(s.part_o + pr * kLat);
+  for (int k = j; k < pieces; k += ways) {
+    const size_t pr = piece_row(r.at, k, h);
+    const float f = exp2f(s.part_ml[pr].x - mx) * inv;
+    const float4* src = reinterpret_cast<const float4*>(s.part_o + pr * kLat);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = axpy4(f, src[c * 32 + lane], acc[c]);
-    }
+    for (int c = 0; c < 4; ++c) acc[c] = axpy4(f, src[c * 32 + lane], acc[c]);
   }
 }
 
 template <int kE>
-__global__ void __launch_bounds__(kE * 4)
+__global__ void __launch_bounds__(kE * 4, 1)
     tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s) {
   constexpr int kThreads = kE * 4, kWarps = kE / 8, kSplit = 128 / kE;
-  constexpr int kRows = kVTok / kWarps;  // a warp's rows of a full tile
+  constexpr int kOwn = kVTok / kWarps;  // a warp's rows of a tile
+  constexpr int kRedLd = kE + 4;
   extern __shared__ __align__(16) uint8_t smem[];
-  auto* so = reinterpret_cast<__nv_bfloat16*>(smem);
-  auto* sl = so + kVTok * kVLd;
-  auto* sw = sl + kVTok * kVLd;
-  auto* part = reinterpret_cast<float4*>(sw + kE * kVLd);  // [warps][128]
-  __shared__ int live[kVTok];
+  auto* rows = reinterpret_cast<__nv_bfloat16*>(smem);  // [2 buffers][high, low][16][kVLd]
+  uint8_t* rest = smem + 2 * kVRows;
+  auto* sw = reinterpret_cast<__nv_bfloat16*>(rest);
+  auto* raw = reinterpret_cast<float4*>(rest);            // [2 pieces][16][128]
+  auto* red = reinterpret_cast<float*>(rest + kVRaw);     // [8][16][kRedLd]
+  auto* part = reinterpret_cast<float4*>(rest + kVRaw);   // [warps][128]
+  static_assert(kWarps * kLat * 4 <= int(value_red(kE)), "the shares of a row fit");
+  __shared__ int live[2][kVTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x / kSplit, e0 = blockIdx.x % kSplit * kE;
   const auto* w =
@@ -1207,96 +1206,138 @@ __global__ void __launch_bounds__(kE * 4)
     cp16(smem_u32(sw + e * kVLd + c), w + size_t(e) * kLat + c, true);
   }
   cp_commit();
+  cp_wait<0>();
+  __syncthreads();
+  // this warp's weights: 8 n-tiles (dims we ..) x 4 steps (columns wk ..)
+  const int we = warp / kVGroups * 64, wk = warp % kVGroups * 64;
+  uint32_t fw[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t r[4];
+    // one ldmatrix: 8 dims x 32 columns, two steps
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      ldsm4(r, smem_u32(sw + (we + 8 * i + (lane & 7)) * kVLd + wk + k * 32 + (lane >> 3) * 8));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) fw[i][4 * k + q] = r[q];
+    }
+  }
+  __syncthreads();
+
   const int tiles = (a.N + kVTok - 1) / kVTok, step = gridDim.y;
-  // rows q = warp, warp + kWarps, .. of a tile; a tile of few rows: several
-  // warps a row
-  Row rows[kRows];
-  auto ways_of = [&](int tile) { return max(kWarps / min(kVTok, a.N - tile * kVTok), 1); };
-  auto row_of = [&](int tile, int k) {
-    const int ways = ways_of(tile);
-    const int n = tile * kVTok + (ways > 1 ? (k == 0 ? warp / ways : kVTok) : warp + k * kWarps);
-    return n < min((tile + 1) * kVTok, a.N) ? n : -1;
-  };
-  auto place = [&](int tile) {
+  // Starts the copies of a tile's rows (a warp copies and joins its own).
+  RowPlace own[kOwn];
+  auto stage = [&](int tile) {
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int n = tile < tiles ? row_of(tile, k) : -1;
-      rows[k].at = n >= 0 ? s.row_info[n] : make_int4(0, 0, 0, 0);
-    }
-  };
-  auto fetch = [&](int tile) {
+    for (int k = 0; k < kOwn; ++k) {
+      const int q = warp + k * kWarps, n = tile * kVTok + q;
+      RowPlace& r = own[k];
+      r.at = tile < tiles && n < a.N ? s.row_info[n] : make_int4(0, 0, 0, 0);
+      if (r.at.x == 1 || r.at.x == 2) {
+        const size_t p0 = piece_row(r.at, 0, h), p1 = piece_row(r.at, 1, h);
+        const float* src = r.at.x == 1 ? s.o + (size_t(n) * kHeads + h) * kLat : s.part_o + p0 * kLat;
+        const uint32_t to = smem_u32(raw + q * 128 + lane);
 #pragma unroll
-    for (int k = 0; k < kRows; ++k)
-      if (tile < tiles && rows[k].at.x > 0) fetch_row(s, row_of(tile, k), h, lane, rows[k]);
-  };
-  place(blockIdx.y);
-  fetch(blockIdx.y);
-  for (int tile = blockIdx.y; tile < tiles; tile += step) {
-    const int n0 = tile * kVTok;
-    const int ways = ways_of(tile);
-    if (ways == 1) {
+        for (int c = 0; c < 4; ++c) cp16(to + c * 512, src + (c * 32 + lane) * 4, true);
+        if (r.at.x == 2) {
+          r.ml0 = s.part_ml[p0];
+          r.ml1 = s.part_ml[p1];
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int q = warp + k * kWarps;
-        float4 acc[4];
-        join_row(s, h, 0, 1, lane, rows[k], acc);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int at = q * kVLd + (c * 32 + lane) * 4;
-          split_store(so + at, sl + at, acc[c]);
+          for (int c = 0; c < 4; ++c)
+            cp16(to + kVTok * kLat * 4 + c * 512, s.part_o + p1 * kLat + (c * 32 + lane) * 4, true);
         }
-        if (lane == 0) live[q] = rows[k].at.x != 0;
-      }
-    } else {
-      const int n_rows = a.N - n0;
-      const int q = warp / ways, j = warp % ways;
-      float4 acc[4];
-      join_row(s, h, j, ways, lane, rows[0], acc);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) part[warp * 128 + c * 32 + lane] = acc[c];
-      if (j == 0 && lane == 0 && q < n_rows) live[q] = rows[0].at.x != 0;
-      __syncthreads();
-      for (int i = tid; i < kVTok * 128; i += kThreads) {
-        const int qq = i >> 7, c = i & 127;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (qq < n_rows)
-          for (int k = 0; k < ways; ++k) {
-            const float4 y = part[(qq * ways + k) * 128 + c];
-            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-          }
-        split_store(so + qq * kVLd + c * 4, sl + qq * kVLd + c * 4, x);
-        if (c == 0 && qq >= n_rows) live[qq] = 0;
       }
     }
-    place(tile + step);
+    cp_commit();
+  };
+  // Joins the staged rows into row buffer buf.
+  auto join = [&](int buf) {
+    cp_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int q = warp + k * kWarps;
+      float4 acc[4];
+      join_row(s, own[k], h, 0, 1, lane, raw + q * 128, acc);
+      __nv_bfloat16* so = rows + (2 * buf * kVTok + q) * kVLd;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        split_store(so + (c * 32 + lane) * 4, so + kVTok * kVLd + (c * 32 + lane) * 4, acc[c]);
+      if (lane == 0) live[buf][q] = own[k].at.x != 0;
+    }
+    __syncwarp();
+  };
+  stage(blockIdx.y);
+  if (tiles == 1 && a.N * 2 <= kWarps) {
+    // fewer rows than warps: several warps a row, each some of its pieces
+    const int ways = kWarps / a.N, q = warp / ways, j = warp % ways;
     cp_wait<0>();
     __syncthreads();
-    fetch(tile + step);
-    float d[4] = {};
-#pragma unroll 4
-    for (int k = 0; k < kLat / 16; k += 2) {
-      uint32_t fa[4], fb[4];
-      // one ldmatrix gives this warp's 8 value dims for two 16-wide steps
-      ldsm4(fb, smem_u32(sw + (warp * 8 + (lane & 7)) * kVLd + k * 16 + (lane >> 3) * 8));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = (lane & 15) * kVLd + (k + i) * 16 + (lane >> 4) * 8;
-        ldsm4(fa, smem_u32(so + at));
-        mma_16816(d, fa, fb[2 * i], fb[2 * i + 1]);
-        ldsm4(fa, smem_u32(sl + at));
-        mma_16816(d, fa, fb[2 * i], fb[2 * i + 1]);
-      }
+    RowPlace r;
+    r.at = q < a.N ? s.row_info[q] : make_int4(0, 0, 0, 0);
+    if (r.at.x == 2) {
+      r.ml0 = s.part_ml[piece_row(r.at, 0, h)];
+      r.ml1 = s.part_ml[piece_row(r.at, 1, h)];
     }
+    float4 acc[4];
+    join_row(s, r, h, j, ways, lane, raw + min(q, kVTok - 1) * 128, acc);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) part[warp * 128 + c * 32 + lane] = acc[c];
+    if (j == 0 && lane == 0 && q < a.N) live[0][q] = r.at.x != 0;
+    __syncthreads();
+    for (int i = tid; i < kVTok * 128; i += kThreads) {
+      const int qq = i >> 7, c = i & 127;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (qq < a.N)
+        for (int k = 0; k < ways; ++k) x = axpy4(1.f, part[(qq * ways + k) * 128 + c], x);
+      split_store(rows + qq * kVLd + c * 4, rows + (kVTok + qq) * kVLd + c * 4, x);
+      if (c == 0 && qq >= a.N) live[0][qq] = 0;
+    }
+  } else {
+    join(0);
+  }
+  stage(blockIdx.y + step);
+  int buf = 0;
+  for (int tile = blockIdx.y; tile < tiles; tile += step, buf ^= 1) {
+    __syncthreads();  // the tile's rows are there, the sums are read
+    float d[8][4] = {};
+    const __nv_bfloat16* so = rows + 2 * buf * kVTok * kVLd;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t fa[4];
+      const int at = (lane & 15) * kVLd + wk + k * 16 + (lane >> 4) * 8;
+      ldsm4(fa, smem_u32(so + at));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma_16816(d[i], fa, fw[i][2 * k], fw[i][2 * k + 1]);
+      ldsm4(fa, smem_u32(so + kVTok * kVLd + at));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma_16816(d[i], fa, fw[i][2 * k], fw[i][2 * k + 1]);
+    }
+    // sum over the warps that share the dims
     const int g = lane >> 2, t = lane & 3;
+    float* mine = red + (warp % kVGroups) * kVTok * kRedLd + we + 2 * t;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int q = g + 8 * half;
-      if (live[q])
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                     size_t(n0 + q) * (kHeads * kVal) + h * kVal + e0 + warp * 8 +
-                                     2 * t) = pack_bf16x2(d[2 * half], d[2 * half + 1]);
+    for (int i = 0; i < 8; ++i) {
+      *reinterpret_cast<float2*>(mine + g * kRedLd + 8 * i) = make_float2(d[i][0], d[i][1]);
+      *reinterpret_cast<float2*>(mine + (g + 8) * kRedLd + 8 * i) = make_float2(d[i][2], d[i][3]);
     }
-    __syncthreads();  // the row buffers are written again
+    if (tile + step < tiles) {
+      join(buf ^ 1);
+      stage(tile + 2 * step);
+    }
+    __syncthreads();
+    {
+      static_assert(kVTok * kE / 4 == kThreads, "four dims of a row per thread");
+      const int q = tid / (kE / 4), e = tid % (kE / 4) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kVGroups; ++k)
+        x = axpy4(1.f, *reinterpret_cast<const float4*>(red + (k * kVTok + q) * kRedLd + e), x);
+      if (live[buf][q])
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                                  size_t(tile * kVTok + q) * (kHeads * kVal) + h * kVal + e0 + e) =
+            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    }
   }
 }
 
