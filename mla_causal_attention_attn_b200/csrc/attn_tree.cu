@@ -182,6 +182,16 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) 
                : "memory");
 }
 
+// Programmatic dependent launch: lets the next kernel of the call start its
+// prologue, and waits until the one before has completed and its writes are
+// visible.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 template <int N>
@@ -248,6 +258,7 @@ template <bool kRope>
 __global__ void __launch_bounds__(kQThreads)
     tree_query_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
                       const __grid_constant__ RopeFreqs f, unsigned int* err_word) {
+  launch_dependents();
   if (blockIdx.y == 0) {
     if (blockIdx.x == 0) {
       if (threadIdx.x == 0) *err_word = 0u;
@@ -613,6 +624,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   cluster_sync();  // both CTAs' barriers are initialised before any remote signal
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  launch_dependents();
+  wait_for_primary();
   Walk walk(a, s, int(blockIdx.x >> 1), int(gridDim.x >> 1));
 
   if (warp == 0 || warp == 2) {
@@ -1101,10 +1114,9 @@ constexpr uint32_t kVRows = 2 * kVTok * kVLd * 2;        // a tile's rows, high 
 constexpr uint32_t kVRaw = 2 * kVTok * kLat * 4;         // the next tile's pieces
 constexpr uint32_t value_red(int e) { return kVGroups * kVTok * (e + 4) * 4; }
 constexpr uint32_t value_smem(int e) {
-  // rows, then the weights at first, the pieces and sums (or the shares of a
-  // row) after that
-  const uint32_t w = e * kVLd * 2, later = kVRaw + value_red(e);
-  return 2 * kVRows + (w > later ? w : later);
+  // the next tile's pieces; the weights at first, the rows and sums after that
+  const uint32_t w = e * kVLd * 2, later = 2 * kVRows + value_red(e);
+  return kVRaw + (w > later ? w : later);
 }
 
 // x as a bf16 and the bf16 of what it leaves: together 2^-17 of x, so that the
@@ -1189,12 +1201,12 @@ __global__ void __launch_bounds__(kE * 4, 1)
   constexpr int kOwn = kVTok / kWarps;  // a warp's rows of a tile
   constexpr int kRedLd = kE + 4;
   extern __shared__ __align__(16) uint8_t smem[];
-  auto* rows = reinterpret_cast<__nv_bfloat16*>(smem);  // [2 buffers][high, low][16][kVLd]
-  uint8_t* rest = smem + 2 * kVRows;
+  auto* raw = reinterpret_cast<float4*>(smem);  // [2 pieces][16][128]
+  uint8_t* rest = smem + kVRaw;
   auto* sw = reinterpret_cast<__nv_bfloat16*>(rest);
-  auto* raw = reinterpret_cast<float4*>(rest);            // [2 pieces][16][128]
-  auto* red = reinterpret_cast<float*>(rest + kVRaw);     // [8][16][kRedLd]
-  auto* part = reinterpret_cast<float4*>(rest + kVRaw);   // [warps][128]
+  auto* rows = reinterpret_cast<__nv_bfloat16*>(rest);      // [2 buffers][high, low][16][kVLd]
+  auto* red = reinterpret_cast<float*>(rest + 2 * kVRows);  // [8][16][kRedLd]
+  auto* part = reinterpret_cast<float4*>(rest + 2 * kVRows);  // [warps][128]
   static_assert(kWarps * kLat * 4 <= int(value_red(kE)), "the shares of a row fit");
   __shared__ int live[2][kVTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1206,24 +1218,6 @@ __global__ void __launch_bounds__(kE * 4, 1)
     cp16(smem_u32(sw + e * kVLd + c), w + size_t(e) * kLat + c, true);
   }
   cp_commit();
-  cp_wait<0>();
-  __syncthreads();
-  // this warp's weights: 8 n-tiles (dims we ..) x 4 steps (columns wk ..)
-  const int we = warp / kVGroups * 64, wk = warp % kVGroups * 64;
-  uint32_t fw[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t r[4];
-    // one ldmatrix: 8 dims x 32 columns, two steps
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      ldsm4(r, smem_u32(sw + (we + 8 * i + (lane & 7)) * kVLd + wk + k * 32 + (lane >> 3) * 8));
-#pragma unroll
-      for (int q = 0; q < 4; ++q) fw[i][4 * k + q] = r[q];
-    }
-  }
-  __syncthreads();
-
   const int tiles = (a.N + kVTok - 1) / kVTok, step = gridDim.y;
   // Starts the copies of a tile's rows (a warp copies and joins its own).
   RowPlace own[kOwn];
@@ -1267,7 +1261,25 @@ __global__ void __launch_bounds__(kE * 4, 1)
     }
     __syncwarp();
   };
+  wait_for_primary();  // (the weights are on their way already)
   stage(blockIdx.y);
+  cp_wait<1>();
+  __syncthreads();
+  // this warp's weights: 8 n-tiles (dims we ..) x 4 steps (columns wk ..)
+  const int we = warp / kVGroups * 64, wk = warp % kVGroups * 64;
+  uint32_t fw[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t r[4];
+    // one ldmatrix: 8 dims x 32 columns, two steps
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      ldsm4(r, smem_u32(sw + (we + 8 * i + (lane & 7)) * kVLd + wk + k * 32 + (lane >> 3) * 8));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) fw[i][4 * k + q] = r[q];
+    }
+  }
+  __syncthreads();
   if (tiles == 1 && a.N * 2 <= kWarps) {
     // fewer rows than warps: several warps a row, each some of its pieces
     const int ways = kWarps / a.N, q = warp / ways, j = warp % ways;
@@ -1341,6 +1353,23 @@ __global__ void __launch_bounds__(kE * 4, 1)
   }
 }
 
+// A launch that may begin while the kernel before it in the stream ends.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 template <int kE>
 cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int y, cudaStream_t stream) {
   static ContextCache attr;
@@ -1348,8 +1377,8 @@ cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int y, cudaStr
   const cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(kern), int(value_smem(kE)), &attr);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(kHeads * 128 / kE, unsigned(y)), kE * 4, value_smem(kE), stream>>>(a, s);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(kHeads * 128 / kE, unsigned(y)), kE * 4, value_smem(kE), stream, a,
+                      s);
 }
 
 }  // namespace
@@ -1389,10 +1418,8 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   static ContextCache attn_attr;
   e = ensure_smem_attr(reinterpret_cast<const void*>(tree_attn_kernel), int(kASmem), &attn_attr);
   if (e != cudaSuccess) return e;
-  tree_attn_kernel<<<2 * clusters, kAThreads, kASmem, stream>>>(
-      tmQ, tmC, a, s, scale_log2, wait_limit_ns, err_word,
-      test_stall);
-  e = cudaGetLastError();
+  e = launch_after(tree_attn_kernel, dim3(2 * clusters), kAThreads, kASmem, stream, tmQ, tmC, a, s,
+                   scale_log2, wait_limit_ns, err_word, test_stall);
   if (e != cudaSuccess) return e;
   return a.N <= 2 * kVTok ? launch_value<64>(a, s, tiles, stream)
                           : launch_value<128>(a, s, tiles < 2 ? tiles : 2, stream);
