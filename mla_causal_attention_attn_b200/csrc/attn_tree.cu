@@ -51,8 +51,24 @@ struct TreeReq {
 };
 static_assert(sizeof(TreeReq) == 32, "TreeReq");
 
+// An item: a piece of a pair.
+struct Item {
+  TreeReq r;
+  int b, pair, t0, t1;
+  int cut_last;  // cut chunk of the last tile, or -1
+  int cut_row;   // its first row without a key
+};
+
+// A cluster's share: its first item and the positions behind that.
+struct Share {
+  long long pos, end;  // pos == end: nothing left; first.t1 == 0: nothing at all
+  Item first;
+};
+static_assert(sizeof(Share) == 72, "Share");
+
 struct Scratch {
   long long* total;    // W
+  Share* share;        // [kMaxClusters]
   TreeReq* req;        // [B]
   int* row_req;        // [N]: the last request that starts at or before the row
   int4* row_info;      // [N]: where the row's results are (RowInfo)
@@ -69,6 +85,8 @@ Scratch carve(void* base, int B, int64_t N) {
   Scratch s;
   s.total = reinterpret_cast<long long*>(p);
   p += 256;
+  s.share = reinterpret_cast<Share*>(p);
+  p += up256(kMaxClusters * sizeof(Share));
   s.req = reinterpret_cast<TreeReq*>(p);
   p += up256(size_t(B) * sizeof(TreeReq));
   s.row_req = reinterpret_cast<int*>(p);
@@ -85,10 +103,48 @@ Scratch carve(void* base, int B, int64_t N) {
   return s;
 }
 
+// Shares there are (none empty), the first position of share c, and the share
+// of position p.
+__device__ __forceinline__ int shares(long long total, int clusters) {
+  return int(min((long long)clusters, total));
+}
+__device__ __forceinline__ long long share_begin(long long total, int c, int clusters) {
+  return total * c / clusters;
+}
+__device__ __forceinline__ int share_of(long long total, long long p, int clusters) {
+  return int(((p + 1) * clusters - 1) / total);
+}
+
+// The item that begins at position pos, of a share that ends at `end`.
+__device__ __noinline__ Item find_item(const TreeReq* req, int B, int page_shift, long long pos,
+                                       long long end) {
+  Item it;
+  int l = 0, h = B;  // the last request whose first position is at or before pos
+  while (h - l > 1) {
+    const int m = (l + h) >> 1;
+    if (req[m].base <= pos) l = m;
+    else h = m;
+  }
+  it.b = l;
+  it.r = req[l];
+  const long long rel = pos - it.r.base;
+  it.pair = int(rel / it.r.tiles);
+  it.t0 = int(rel - (long long)it.pair * it.r.tiles);
+  it.t1 = int(min((long long)it.r.tiles, it.t0 + (end - pos)));
+  // The chunk of 64 keys that the request's last key lies in has rows to be
+  // zeroed when a TMA box (min(page, 64) rows) goes past that key.
+  const int box = page_shift >= 6 ? 64 : 1 << page_shift;
+  it.cut_last = -1;
+  it.cut_row = it.r.keys & 63;
+  if (it.t1 == it.r.tiles && (it.r.keys & (box - 1)) != 0)
+    it.cut_last = ((it.r.keys - 1) & (kTileKeys - 1)) >> 6;
+  return it;
+}
+
 // Lays the requests out (one CTA). Lengths are made safe: rows inside [0, N]
 // and, by a running maximum of the starts, in one request at most; keys inside
 // the request's table.
-__device__ void schedule(const AttnTreeArgs& a, const Scratch& s) {
+__device__ void schedule(const AttnTreeArgs& a, const Scratch& s, int clusters) {
   __shared__ long long warp_sum[8];
   __shared__ int warp_max[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -137,18 +193,18 @@ __device__ void schedule(const AttnTreeArgs& a, const Scratch& s) {
     base += all;
   }
   if (threadIdx.x == 0) *s.total = base;
-}
-
-// Shares there are (none empty), the first position of share c, and the share
-// of position p.
-__device__ __forceinline__ int shares(long long total, int clusters) {
-  return int(min((long long)clusters, total));
-}
-__device__ __forceinline__ long long share_begin(long long total, int c, int clusters) {
-  return total * c / clusters;
-}
-__device__ __forceinline__ int share_of(long long total, long long p, int clusters) {
-  return int(((p + 1) * clusters - 1) / total);
+  __syncthreads();  // (the requests are read back below)
+  const int n = shares(base, clusters);
+  for (int c = threadIdx.x; c < clusters; c += blockDim.x) {
+    Share sh{};
+    if (c < n) {
+      sh.pos = share_begin(base, c, n);
+      sh.end = share_begin(base, c + 1, n);
+      sh.first = find_item(s.req, a.B, a.page_shift, sh.pos, sh.end);
+      sh.pos += sh.first.t1 - sh.first.t0;
+    }
+    s.share[c] = sh;
+  }
 }
 
 // ---------------------------------------------------------------- fragments
@@ -257,12 +313,12 @@ __device__ void rotate_queries(const AttnTreeArgs& a, const Scratch& s, const Ro
 template <bool kRope>
 __global__ void __launch_bounds__(kQThreads)
     tree_query_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
-                      const __grid_constant__ RopeFreqs f, unsigned int* err_word) {
+                      const __grid_constant__ RopeFreqs f, int clusters, unsigned int* err_word) {
   launch_dependents();
   if (blockIdx.y == 0) {
     if (blockIdx.x == 0) {
       if (threadIdx.x == 0) *err_word = 0u;
-      schedule(a, s);
+      schedule(a, s, clusters);
     } else {
       rotate_queries<kRope>(a, s, f, blockIdx.x - 1, gridDim.x - 1);
     }
@@ -369,7 +425,7 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // applied by a rolled pass over the few tiles that need one.
 //
 // Every wait is bounded; the teardown is the pair kernel's of attn_prefill.cu.
-constexpr int kAThreads = 320;
+constexpr int kAThreads = 416;
 constexpr uint32_t kBlk = 16384;                 // ring block
 constexpr int kKRing = 4, kVRing = 3;
 constexpr int kKBlocks = kRow / 64;              // 9 K blocks a tile
@@ -382,49 +438,6 @@ constexpr size_t kASmem = kOffV + kVRing * kBlk + 1024;
 static_assert(kASmem <= 225 * 1024, "shared memory budget");
 constexpr uint32_t kColO = 0, kColS = 256;       // tensor memory columns
 constexpr float kRescale = 8.f;                  // log2 growth of the maximum that rescales O
-
-// An item: a piece of a pair.
-struct Item {
-  TreeReq r;
-  int b, pair, t0, t1;
-  int cut_last;  // cut chunk of the last tile, or -1
-  int cut_row;   // its first row without a key
-};
-
-// The item that begins at position pos, of a share that ends at `end`.
-__device__ __noinline__ Item find_item(const TreeReq* req, int B, int page_shift, long long pos,
-                                       long long end) {
-  Item it;
-  int l = 0, h = B;  // the last request whose first position is at or before pos
-  while (h - l > 1) {
-    const int m = (l + h) >> 1;
-    if (req[m].base <= pos) l = m;
-    else h = m;
-  }
-  it.b = l;
-  it.r = req[l];
-  const long long rel = pos - it.r.base;
-  it.pair = int(rel / it.r.tiles);
-  it.t0 = int(rel - (long long)it.pair * it.r.tiles);
-  it.t1 = int(min((long long)it.r.tiles, it.t0 + (end - pos)));
-  // The chunk of 64 keys that the request's last key lies in has rows to be
-  // zeroed when a TMA box (min(page, 64) rows) goes past that key.
-  const int box = page_shift >= 6 ? 64 : 1 << page_shift;
-  it.cut_last = -1;
-  it.cut_row = it.r.keys & 63;
-  if (it.t1 == it.r.tiles && (it.r.keys & (box - 1)) != 0)
-    it.cut_last = ((it.r.keys - 1) & (kTileKeys - 1)) >> 6;
-  return it;
-}
-
-// A cluster's share: positions [x, y).
-__device__ __noinline__ longlong2 find_share(const long long* total_at, int cluster, int clusters) {
-  const long long total = *total_at;
-  clusters = shares(total, clusters);
-  if (cluster >= clusters) return make_longlong2(0, 0);
-  return make_longlong2(share_begin(total, cluster, clusters),
-                        share_begin(total, cluster + 1, clusters));
-}
 
 // Where row n's latent results are: x pieces (0: the row belongs to no request,
 // 1: whole, in Scratch::o, -1: a request without keys), y the slot of the first
@@ -456,20 +469,24 @@ struct Walk {
   int next_slot;
   int item_no;   // items begun so far - 1
 
-  __device__ __forceinline__ Walk(const AttnTreeArgs& aa, const Scratch& ss, int cluster,
-                                  int clusters)
+  __device__ __forceinline__ Walk(const AttnTreeArgs& aa, const Scratch& ss, int cluster)
       : a(&aa), s(&ss), tile(0), next_slot(2 * cluster), item_no(-1) {
-    const longlong2 share = find_share(ss.total, cluster, clusters);
-    pos = share.x;
-    end = share.y;
+    const Share& share = ss.share[cluster];
+    it = share.first;
+    pos = share.pos;
+    end = share.end;
   }
   // Moves to the next tile; false at the end.
   __device__ __forceinline__ bool next() {
-    if (item_no >= 0 && ++tile < it.t1) return true;
-    if (pos >= end) return false;
-    it = find_item(s->req, a->B, a->page_shift, pos, end);
+    if (item_no >= 0) {
+      if (++tile < it.t1) return true;
+      if (pos >= end) return false;
+      it = find_item(s->req, a->B, a->page_shift, pos, end);
+      pos += it.t1 - it.t0;
+    } else if (it.t1 == 0) {
+      return false;
+    }
     tile = it.t0;
-    pos += it.t1 - it.t0;
     slot = it.t0 == 0 && it.t1 == it.r.tiles ? -1 : next_slot;
     next_slot |= 1;
     ++item_no;
@@ -519,6 +536,31 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
                                           uint32_t site) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_more(bar, parity, w, site));
+}
+
+// The pair's MMA and commit, issued by the lane with el != 0. The issuing warp
+// runs as a whole, its waits voted: descriptors and addresses then stay in
+// uniform registers and a block's wait, four MMAs and commit take no longer
+// than the MMAs (258 clocks measured; one thread alone took 480).
+__device__ __forceinline__ void mma_pair_el(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(el)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_pair_el(uint32_t bar, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(bar),
+      "h"(uint16_t(0x3)), "r"(el)
+      : "memory");
 }
 
 __device__ __forceinline__ void fence_acq_rel_cluster() {
@@ -574,8 +616,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   __shared__ uint64_t cut_full[2];    // this CTA's cut V block of product m landed
   __shared__ uint64_t drain_bar[2];   // the two issuers' products in flight
   __shared__ uint64_t never_bar;      // no thread ever arrives (failure-detection test)
-  __shared__ uint32_t n_issued[3];    // K, V and query blocks this CTA's producers issued
-  __shared__ uint32_t n_cut[2];       // cut blocks issued, reported
+  __shared__ uint32_t n_issued[5];    // blocks this CTA's producers issued: K (2), V (2), query
+  __shared__ uint32_t n_cut[3];       // cut blocks issued (by product), reported
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float xch[2][2][64];     // maxima of a row's two halves, by parity of the tile
@@ -590,7 +632,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    n_issued[0] = n_issued[1] = n_issued[2] = n_cut[0] = n_cut[1] = 0;
+    for (int i = 0; i < 5; ++i) n_issued[i] = 0;
+    for (int i = 0; i < 3; ++i) n_cut[i] = 0;
     for (int i = 0; i < kKRing; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -626,13 +669,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   const uint32_t tmem = tmem_slot;
   launch_dependents();
   wait_for_primary();
-  Walk walk(a, s, int(blockIdx.x >> 1), int(gridDim.x >> 1));
+  Walk walk(a, s, int(blockIdx.x >> 1));
 
-  if (warp == 0 || warp == 2) {
+  if (warp == 0 || warp == 11 || warp == 2 || warp == 12) {
     // ------------------------------------------------------------ producers
-    // warp 0: query and K blocks, warp 2: V blocks. All lanes: one TMA copy
-    // each (a block is 2 to 8 pieces of pages); lane i knows the page of box i
-    // of the tile.
+    // warps 0 and 11: K blocks, warps 2 and 12: V blocks, every other one each
+    // (a block's wait, arming and copies take one warp 600 to 1000 clocks, more
+    // than the 485 or 546 that its products take). All lanes: one TMA copy each
+    // (a block is 2 to 8 pieces of pages); lane i knows the page of box i of the
+    // tile.
     if (lane == 0) {
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmC);
@@ -640,142 +685,138 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     const int box_shift = a.page_shift >= 6 ? 6 : a.page_shift;
     const int per = 64 >> box_shift;  // boxes a 64-key chunk
     const int pmask = (1 << a.page_shift) - 1;
+    const int odd = warp >= 11 ? 1 : 0;
     auto page_at = [&](int key) -> int {  // page, or one past the last: zeros
       const int id = key < walk.it.r.keys ? page_of(a, walk.it.b, key) : -1;
       return id >= 0 ? id : a.num_pages;
     };
     uint32_t issued = 0;
     bool ok = true;
-    if (warp == 0) {
+    if (warp == 0 || warp == 11) {
       RingPos<kKRing> pos;
-      uint32_t q_issued = 0;
+      if (odd) pos.advance();
       const uint32_t full0 = mapa_shared(smem_u32(&k_full[0]), 0);
-      const uint32_t q_full0 = mapa_shared(smem_u32(&q_full[0]), 0);
+      int i = odd;  // the block of the tile
       while (ok && walk.next()) {
         const int key = walk.tile * kTileKeys + int(rank) * 128 + (lane << box_shift);
         const int page = lane < 2 * per ? page_at(key) : 0;
-        const bool first = walk.first();
-        const int node = 2 * walk.it.pair + int(rank);
-        const int qrow =
-            node < walk.it.r.nodes ? (walk.it.r.start + node) * kHeads : a.N * kHeads;  // zeros
+        const int row = key & pmask;
+        uint8_t* dst = smem + kOffRing + (lane << box_shift) * 128;
 #pragma unroll 1
-        for (int i = 0; ok && i < kKBlocks; ++i) {
-          if (first) {
-            ok = wait_warp(&q_empty[i], uint32_t(walk.item_no & 1) ^ 1u, waits, 2);
-            if (!ok) break;
-            ++q_issued;
-            if (lane == 0) {
-              if (leader) mbar_arrive_expect_tx(&q_full[i], 2 * kQBlk);
-              n_issued[2] = q_issued;
-              tma_load_2d_pair(smem + i * kQBlk, &tmQ, q_full0 + i * 8, i * 64, qrow);
-            }
-          }
+        for (; i < kKBlocks; i += 2) {
           ok = wait_warp(&k_empty[pos.slot], pos.par ^ 1u, waits, 1);
           if (!ok) break;
           ++issued;
           // (bytes that land before the barrier is armed are counted all the same)
           if (lane == 0) {
             if (leader) mbar_arrive_expect_tx(&k_full[pos.slot], 2 * kBlk);
-            n_issued[0] = issued;
+            n_issued[odd] = issued;
           }
           if (lane < 2 * per)
-            tma_load_3d_pair(smem + kOffRing + pos.slot * kBlk + (lane << box_shift) * 128, &tmC,
-                             full0 + pos.slot * 8, i * 64, key & pmask, page);
+            tma_load_3d_pair(dst + pos.slot * kBlk, &tmC, full0 + pos.slot * 8, i * 64, row, page);
+          pos.advance();
           pos.advance();
         }
+        i -= kKBlocks;
       }
     } else {
       RingPos<kVRing> pos;
+      if (odd) pos.advance();
       const uint32_t full0 = mapa_shared(smem_u32(&v_full[0]), 0);
-      const uint32_t cut0 = mapa_shared(smem_u32(&cut_full[0]), rank);
+      const uint32_t cut0 = mapa_shared(smem_u32(&cut_full[odd]), rank);
       const int vi = lane & (per - 1), vj = lane >> (6 - box_shift);  // box, 64-column half
+      const int col = odd * 256 + int(rank) * 128 + vj * 64;          // (block i: product m = i % 2)
+      uint8_t* dst = smem + kOffV + vj * 8192 + (vi << box_shift) * 128;
       uint32_t cuts = 0;
       while (ok && walk.next()) {
         const int tile_key = walk.tile * kTileKeys;
         const int pages = lane < 4 * per ? page_at(tile_key + (lane << box_shift)) : 0;
         const int cut = walk.cut();
 #pragma unroll 1
-        for (int i = 0; i < kVBlocks; ++i) {
-          const int c = i >> 1, m = i & 1;
+        for (int c = 0; c < 4; ++c) {
           const int page = __shfl_sync(0xffffffffu, pages, c * per + vi);
           ok = wait_warp(&v_empty[pos.slot], pos.par ^ 1u, waits, 3);
           if (!ok) break;
           ++issued;
           if (lane == 0) {
             if (leader) mbar_arrive_expect_tx(&v_full[pos.slot], 2 * kBlk);
-            n_issued[1] = issued;
+            n_issued[2 + odd] = issued;
           }
           uint32_t bar = full0 + pos.slot * 8;
           if (c == cut) {
             ++cuts;
             if (lane == 0) {
-              mbar_arrive_expect_tx(&cut_full[m], kBlk);
-              n_cut[0] = cuts;
+              mbar_arrive_expect_tx(&cut_full[odd], kBlk);
+              n_cut[odd] = cuts;
             }
-            bar = cut0 + m * 8;
+            bar = cut0;
           }
           if (lane < 2 * per)
-            tma_load_3d_pair(smem + kOffV + pos.slot * kBlk + vj * 8192 + (vi << box_shift) * 128,
-                             &tmC, bar, m * 256 + int(rank) * 128 + vj * 64,
+            tma_load_3d_pair(dst + pos.slot * kBlk, &tmC, bar, col,
                              (tile_key + c * 64 + (vi << box_shift)) & pmask, page);
+          pos.advance();
           pos.advance();
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ score products (even CTA)
-    if (lane == 0 && leader) {
+    if (leader) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, 256, false, false);
+      const uint32_t el = elect_one() ? 1u : 0u;
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem) + kOffRing, 16, 1024);
+      const uint32_t empty0 = smem_u32(&k_empty[0]), q_empty0 = smem_u32(&q_empty[0]);
       RingPos<kKRing> pos;
       bool ok = true, any = false;
       for (int g = 0; ok && walk.next(); ++g) {
         const bool first = walk.first(), last = walk.last();
         const uint32_t d = tmem + kColS + 128u * uint32_t(g & 1);
-        if (g >= 2) ok = wait_more(&s_free[g & 1], uint32_t((g >> 1) - 1) & 1u, waits, 6);
+        if (g >= 2) ok = wait_warp(&s_free[g & 1], uint32_t((g >> 1) - 1) & 1u, waits, 6);
 #pragma unroll 1
         for (int i = 0; ok && i < kKBlocks; ++i) {
-          if (first) ok = wait_more(&q_full[i], uint32_t(walk.item_no & 1), waits, 5);
-          ok = ok && wait_bar(&k_full[pos.slot], pos.par, waits, 4);
+          if (first) ok = wait_warp(&q_full[i], uint32_t(walk.item_no & 1), waits, 5);
+          ok = ok && wait_warp(&k_full[pos.slot], pos.par, waits, 4);
           if (!ok) break;
           tc_fence_after();
           const uint64_t qd = q_desc + i * (kQBlk >> 4);
           const uint64_t kd = k_desc + pos.slot * (kBlk >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss_pair(d, qd + kk * 2, kd + kk * 2, idesc, (i | kk) != 0 ? 1u : 0u);
+            mma_pair_el(d, qd + kk * 2, kd + kk * 2, idesc, (i | kk) != 0 ? 1u : 0u, el);
           any = true;
-          mma_commit_pair_mc(&k_empty[pos.slot], 0x3);
-          if (last) mma_commit_pair_mc(&q_empty[i], 0x3);
+          commit_pair_el(empty0 + pos.slot * 8, el);
+          if (last) commit_pair_el(q_empty0 + i * 8, el);
           pos.advance();
         }
-        if (ok) mma_commit_pair_mc(&s_full[g & 1], 0x3);
+        if (ok) commit_pair_el(smem_u32(&s_full[g & 1]), el);
       }
       if (!ok && any) {
-        mma_commit_pair_mc(&drain_bar[0], 0x1);
+        commit_pair_el(smem_u32(&drain_bar[0]), el);
         int zero = 0;
-        wait_more(&drain_bar[0], 0, Waits{&zero, err_word, wait_limit_ns}, 10);
+        wait_warp(&drain_bar[0], 0, Waits{&zero, err_word, wait_limit_ns}, 10);
       }
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ value products (even CTA)
-    if (lane == 0 && leader) {
+    if (leader) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, 256, false, true);
+      const uint32_t el = elect_one() ? 1u : 0u;
       const uint64_t p_desc = sdesc_sw128(smem_u32(smem) + kOffP, 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem) + kOffV, 8192, 1024);
+      const uint32_t empty0 = smem_u32(&v_empty[0]), p_free0 = smem_u32(&p_free[0]);
       RingPos<kVRing> pos;
       bool ok = true, any = false;
       for (int g = 0; ok && walk.next(); ++g) {
         const bool first = walk.first();
         const int cut = walk.cut();
-        ok = wait_more(&p_full[0], uint32_t(g) & 1u, waits, 7);
+        ok = wait_warp(&p_full[0], uint32_t(g) & 1u, waits, 7);
         if (first && walk.item_no > 0)
-          ok = ok && wait_more(&o_free, uint32_t(walk.item_no - 1) & 1u, waits, 8);
+          ok = ok && wait_warp(&o_free, uint32_t(walk.item_no - 1) & 1u, waits, 8);
 #pragma unroll 1
         for (int i = 0; ok && i < kVBlocks; ++i) {
-          if (i == 4) ok = wait_more(&p_full[1], uint32_t(g) & 1u, waits, 9);
-          ok = ok && wait_bar(&v_full[pos.slot], pos.par, waits, 14);
+          if (i == 4) ok = wait_warp(&p_full[1], uint32_t(g) & 1u, waits, 9);
+          ok = ok && wait_warp(&v_full[pos.slot], pos.par, waits, 14);
           if (!ok) break;
           const int c = i >> 1, m = i & 1;
           if (c == cut) fence_acq_rel_cluster();  // (reported by a thread of either CTA)
@@ -785,18 +826,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
           const uint64_t vd = v_desc + pos.slot * (kBlk >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss_pair(d, pd + kk * 2, vd + kk * (16 * 128 >> 4), idesc,
-                        (!first || c > 0 || kk > 0) ? 1u : 0u);
+            mma_pair_el(d, pd + kk * 2, vd + kk * (16 * 128 >> 4), idesc,
+                        (!first || c > 0 || kk > 0) ? 1u : 0u, el);
           any = true;
-          mma_commit_pair_mc(&v_empty[pos.slot], 0x3);
-          if ((i & 3) == 3) mma_commit_pair_mc(&p_free[i >> 2], 0x3);
+          commit_pair_el(empty0 + pos.slot * 8, el);
+          if ((i & 3) == 3) commit_pair_el(p_free0 + (i >> 2) * 8, el);
           pos.advance();
         }
       }
       if (!ok && any) {
-        mma_commit_pair_mc(&drain_bar[1], 0x1);
+        commit_pair_el(smem_u32(&drain_bar[1]), el);
         int zero = 0;
-        wait_more(&drain_bar[1], 0, Waits{&zero, err_word, wait_limit_ns}, 18);
+        wait_warp(&drain_bar[1], 0, Waits{&zero, err_word, wait_limit_ns}, 18);
+      }
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ query blocks
+    if (lane == 0) {
+      const uint32_t full0 = mapa_shared(smem_u32(&q_full[0]), 0);
+      uint32_t issued = 0;
+      bool ok = true;
+      while (ok && walk.next()) {
+        if (!walk.first()) continue;
+        const int node = 2 * walk.it.pair + int(rank);
+        const int row =
+            node < walk.it.r.nodes ? (walk.it.r.start + node) * kHeads : a.N * kHeads;  // zeros
+#pragma unroll 1
+        for (int i = 0; i < kKBlocks; ++i) {
+          ok = wait_more(&q_empty[i], uint32_t(walk.item_no & 1) ^ 1u, waits, 2);
+          if (!ok) break;
+          if (leader) mbar_arrive_expect_tx(&q_full[i], 2 * kQBlk);
+          n_issued[4] = ++issued;
+          tma_load_2d_pair(smem + i * kQBlk, &tmQ, full0 + i * 8, i * 64, row);
+        }
       }
     }
   } else if (warp == 8) {
@@ -841,7 +903,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
           __syncwarp();
           ++cuts;
           if (lane == 0) {
-            n_cut[1] = cuts;
+            n_cut[2] = cuts;
             mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
           }
         }
@@ -1046,47 +1108,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   // Without an abort every block that was issued has been read by a product.
   const bool aborted =
       abort_flag != 0 || ld_shared_cluster_u32(mapa_shared(smem_u32(&abort_flag), rank ^ 1)) != 0;
-  if (aborted && warp == 9 && lane == 0 && n_cut[1] < n_cut[0]) {
-    // cut blocks that were issued but not reported (after an abort): they land
-    // on this CTA's barriers, then count on the even CTA's
+  if (aborted && warp == 9 && lane == 0) {
+    // cut blocks that were issued but not reported: they land on this CTA's
+    // barriers, then count on the even CTA's
     int zero = 0;
     const Waits drain{&zero, err_word, wait_limit_ns};
-    Walk w(a, s, int(blockIdx.x >> 1), int(gridDim.x >> 1));
-    uint32_t cuts = 0;
-    for (int g = 0; cuts < n_cut[0] && w.next(); ++g) {
+    Walk w(a, s, int(blockIdx.x >> 1));
+    const uint32_t all = n_cut[0] + n_cut[1];
+    uint32_t item = 0;  // items with a cut so far
+    for (int g = 0; 2 * item < all && w.next(); ++g) {
       const int cut = w.cut();
-      for (int k = 0; cut >= 0 && k < 2 && cuts < n_cut[0]; ++k, ++cuts)
-        if (cuts >= n_cut[1]) {
-          const uint32_t slot = (uint32_t(g) * kVBlocks + 2 * cut + k) % kVRing;
-          wait_more(&cut_full[k], (cuts >> 1) & 1u, drain, 16);
+      if (cut < 0) continue;
+      for (int m = 0; m < 2; ++m)
+        if (item < n_cut[m] && 2 * item + m >= n_cut[2]) {
+          const uint32_t slot = (uint32_t(g) * kVBlocks + 2 * cut + m) % kVRing;
+          wait_more(&cut_full[m], item & 1u, drain, 16);
           mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
         }
+      ++item;
     }
   }
   __syncwarp();
   if (aborted) cluster_sync();
   if (aborted && leader && warp == 0 && lane == 0) {
-    // Account for blocks that only one CTA issued (possible only after an
-    // abort), then wait for the last phase of every slot.
+    // Account for blocks that only one CTA issued, then wait for the last phases
+    // of every slot. Producer `which` of a ring issued the blocks which % 2,
+    // which % 2 + 2, ...; the query blocks have one producer.
     int zero = 0;
     const Waits drain{&zero, err_word, wait_limit_ns};
-    for (int which = 0; which < 3; ++which) {
-      uint64_t* bars = which == 0 ? k_full : which == 1 ? v_full : q_full;
-      const uint32_t ring = which == 0 ? kKRing : which == 1 ? kVRing : kKBlocks;
-      const uint32_t bytes = which == 2 ? kQBlk : kBlk;
-      const uint32_t own = n_issued[which];
-      const uint32_t peer = ld_shared_cluster_u32(mapa_shared(smem_u32(&n_issued[which]), 1));
-      const uint32_t lo = min(own, peer), hi = max(own, peer);
-      for (uint32_t i = lo; i < hi; ++i) {
-        uint64_t* fb = &bars[i % ring];
-        if (i < own)  // armed for both CTAs' bytes, the odd CTA's copy never came
-          mbar_complete_tx_cluster(mapa_shared(smem_u32(fb), 0), bytes);
-        else          // the odd CTA's copy came, this CTA never armed the phase
-          mbar_arrive_expect_tx(fb, bytes);
+    for (int pass = 0; pass < 2; ++pass)
+      for (int which = 0; which < 5; ++which) {
+        uint64_t* bars = which < 2 ? k_full : which < 4 ? v_full : q_full;
+        const uint32_t ring = which < 2 ? kKRing : which < 4 ? kVRing : kKBlocks;
+        const uint32_t bytes = which == 4 ? kQBlk : kBlk;
+        const uint32_t stride = which == 4 ? 1 : 2, off = which == 4 ? 0 : which & 1;
+        const uint32_t own = n_issued[which];
+        const uint32_t peer = ld_shared_cluster_u32(mapa_shared(smem_u32(&n_issued[which]), 1));
+        const uint32_t lo = min(own, peer), hi = max(own, peer);
+        for (uint32_t k = pass == 0 ? lo : (hi > ring ? hi - ring : 0); k < hi; ++k) {
+          const uint32_t n = k * stride + off;
+          uint64_t* fb = &bars[n % ring];
+          if (pass == 1)
+            wait_more(fb, (n / ring) & 1u, drain, 17);
+          else if (k < own)  // armed for both CTAs' bytes, the odd CTA's copy never came
+            mbar_complete_tx_cluster(mapa_shared(smem_u32(fb), 0), bytes);
+          else               // the odd CTA's copy came, this CTA never armed the phase
+            mbar_arrive_expect_tx(fb, bytes);
+        }
       }
-      for (uint32_t i = hi > ring ? hi - ring : 0; i < hi; ++i)
-        wait_more(&bars[i % ring], (i / ring) & 1u, drain, 17);
-    }
   }
   // Last barrier: no copy is in flight toward either CTA; neither leaves, nor
   // frees the pair's tensor memory, before both get here.
@@ -1384,7 +1453,7 @@ cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int y, cudaStr
 }  // namespace
 
 size_t attn_tree_scratch_bytes(int B, int64_t N) {
-  return 256 + up256(size_t(B) * sizeof(TreeReq)) + up256(size_t(N) * 4) + up256(size_t(N) * 16) + up256(size_t(N) * kHeads * kRow * 2) +
+  return 256 + up256(kMaxClusters * sizeof(Share)) + up256(size_t(B) * sizeof(TreeReq)) + up256(size_t(N) * 4) + up256(size_t(N) * 16) + up256(size_t(N) * kHeads * kRow * 2) +
          up256(size_t(N) * kHeads * kLat * 4) + up256(size_t(kMaxSlots) * 128 * sizeof(float2)) +
          size_t(kMaxSlots) * 128 * kLat * 4;
 }
@@ -1408,9 +1477,9 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   const int tiles = (a.N + kQTok - 1) / kQTok;
   const dim3 qgrid(kHeads * 4, unsigned(tiles < 3 ? tiles : 3) + 1);
   if (rotary)
-    tree_query_kernel<true><<<qgrid, kQThreads, 0, stream>>>(a, s, *rotary, err_word);
+    tree_query_kernel<true><<<qgrid, kQThreads, 0, stream>>>(a, s, *rotary, clusters, err_word);
   else
-    tree_query_kernel<false><<<qgrid, kQThreads, 0, stream>>>(a, s, RopeFreqs{}, err_word);
+    tree_query_kernel<false><<<qgrid, kQThreads, 0, stream>>>(a, s, RopeFreqs{}, clusters, err_word);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   float scale_log2 = a.scale * 1.4426950408889634f;
