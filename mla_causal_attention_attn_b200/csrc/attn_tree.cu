@@ -411,9 +411,12 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // has row t % 64 and 128 of the keys; both threads of a row keep one running
 // maximum.
 //
-// Signals across the pair cost about 0.7 us for the arriving thread, so they
-// come from helper threads of the odd CTA: P ready (per half of the keys), S
-// read, O read. Ring copies of both CTAs complete on the even CTA's barriers.
+// The odd CTA's softmax warps arrive on the even CTA's barriers themselves (P
+// ready, S read, O read), with a release at CTA scope: what such an arrival
+// orders is read by the arriving CTA's own tensor core (a release at cluster
+// scope held the arriving thread for about 0.7 us, and a helper thread that
+// forwarded the arrivals added as much to every tile). Ring copies of both CTAs
+// complete on the even CTA's barriers.
 // Rows behind the request's last key are zeroed in the V blocks of the last
 // 64-key chunk (0 * NaN is NaN): those two blocks complete on a barrier of
 // their own CTA, a warp zeroes the rows and then reports the bytes to the ring.
@@ -425,7 +428,7 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // applied by a rolled pass over the few tiles that need one.
 //
 // Every wait is bounded; the teardown is the pair kernel's of attn_prefill.cu.
-constexpr int kAThreads = 416;
+constexpr int kAThreads = 384;
 constexpr uint32_t kBlk = 16384;                 // ring block
 constexpr int kKRing = 4, kVRing = 3;
 constexpr int kKBlocks = kRow / 64;              // 9 K blocks a tile
@@ -563,6 +566,12 @@ __device__ __forceinline__ void commit_pair_el(uint32_t bar, uint32_t el) {
       : "memory");
 }
 
+// Arrive on the even CTA's barrier at the offset of `bar`, release at CTA scope.
+__device__ __forceinline__ void arrive_even(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
+               : "memory");
+}
+
 __device__ __forceinline__ void fence_acq_rel_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
@@ -608,11 +617,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   __shared__ uint64_t q_full[kKBlocks];   // even CTA: both CTAs' query blocks landed
   __shared__ uint64_t q_empty[kKBlocks];  // the item's last score product has read the block
   __shared__ uint64_t s_full[2];      // scores are in buffer b
-  __shared__ uint64_t s_free[2];      // even CTA: read by both CTAs; odd CTA: by its own warps
-  __shared__ uint64_t p_full[2];      // even CTA: P of key half h of both CTAs; odd CTA: its own;
-                                      // [0] also waits for the other warps' part of O's rescaling
+  __shared__ uint64_t s_free[2];      // even CTA: both CTAs have read buffer b
+  __shared__ uint64_t p_full[2];      // even CTA: P of key half h of both CTAs is there; [0]: so
+                                      // is the other warps' part of O's rescaling
   __shared__ uint64_t p_free[2];      // the value products have read P of key half h
-  __shared__ uint64_t o_free;         // O of an item is read (even / odd as s_free)
+  __shared__ uint64_t o_free;         // even CTA: both CTAs have read O of an item
   __shared__ uint64_t cut_full[2];    // this CTA's cut V block of product m landed
   __shared__ uint64_t drain_bar[2];   // the two issuers' products in flight
   __shared__ uint64_t never_bar;      // no thread ever arrives (failure-detection test)
@@ -648,13 +657,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], leader ? 5 : 4);
-      mbar_init(&p_full[i], (i == 0 ? 4 : 2) + (leader ? 1 : 0));
+      mbar_init(&s_free[i], 8);
+      mbar_init(&p_full[i], i == 0 ? 8 : 4);
       mbar_init(&p_free[i], 1);
       mbar_init(&cut_full[i], 1);
       mbar_init(&drain_bar[i], 1);
     }
-    mbar_init(&o_free, leader ? 5 : 4);
+    mbar_init(&o_free, 8);
     mbar_init(&never_bar, 1);
     fence_barrier_init();
   }
@@ -671,9 +680,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   wait_for_primary();
   Walk walk(a, s, int(blockIdx.x >> 1));
 
-  if (warp == 0 || warp == 11 || warp == 2 || warp == 12) {
+  if (warp == 0 || warp == 10 || warp == 2 || warp == 11) {
     // ------------------------------------------------------------ producers
-    // warps 0 and 11: K blocks, warps 2 and 12: V blocks, every other one each
+    // warps 0 and 10: K blocks, warps 2 and 11: V blocks, every other one each
     // (a block's wait, arming and copies take one warp 600 to 1000 clocks, more
     // than the 485 or 546 that its products take). All lanes: one TMA copy each
     // (a block is 2 to 8 pieces of pages); lane i knows the page of box i of the
@@ -685,14 +694,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     const int box_shift = a.page_shift >= 6 ? 6 : a.page_shift;
     const int per = 64 >> box_shift;  // boxes a 64-key chunk
     const int pmask = (1 << a.page_shift) - 1;
-    const int odd = warp >= 11 ? 1 : 0;
+    const int odd = warp >= 10 ? 1 : 0;
     auto page_at = [&](int key) -> int {  // page, or one past the last: zeros
       const int id = key < walk.it.r.keys ? page_of(a, walk.it.b, key) : -1;
       return id >= 0 ? id : a.num_pages;
     };
     uint32_t issued = 0;
     bool ok = true;
-    if (warp == 0 || warp == 11) {
+    if (warp == 0 || warp == 10) {
       RingPos<kKRing> pos;
       if (odd) pos.advance();
       const uint32_t full0 = mapa_shared(smem_u32(&k_full[0]), 0);
@@ -840,7 +849,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         wait_warp(&drain_bar[1], 0, Waits{&zero, err_word, wait_limit_ns}, 18);
       }
     }
-  } else if (warp == 10) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------ query blocks
     if (lane == 0) {
       const uint32_t full0 = mapa_shared(smem_u32(&q_full[0]), 0);
@@ -862,29 +871,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       }
     }
   } else if (warp == 8) {
-    // ------------------------------------------------------------ helper (odd CTA): P
-    // (even CTA: the rows' places for the value kernel)
-    if (leader) {
+    // ------------------------------------------------------------ rows' places, cut blocks
+    if (leader)
       for (int n = int(blockIdx.x >> 1) * 32 + lane; n < a.N; n += int(gridDim.x >> 1) * 32)
         s.row_info[n] = place_of(s, int(gridDim.x >> 1), n);
-    } else if (lane == 0) {
-      bool ok = true;
-      for (int g = 0; ok && walk.next(); ++g)
-#pragma unroll 1
-        for (int h = 0; ok && h < 2; ++h) {
-          ok = wait_more(&p_full[h], uint32_t(g) & 1u, waits, 11);
-          if (ok) mbar_arrive_cluster(mapa_shared(smem_u32(&p_full[h]), 0));
-        }
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ helper: S, O, cut blocks
+    __syncwarp();
     bool ok = true;
     uint32_t cuts = 0;
     for (int g = 0; ok && walk.next(); ++g) {
-      if (!leader) {
-        ok = wait_warp(&s_free[g & 1], uint32_t(g >> 1) & 1u, waits, 12);
-        if (ok && lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_free[g & 1]), 0));
-      }
       const int cut = walk.cut();
       if (cut >= 0)
 #pragma unroll 1
@@ -907,10 +901,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
             mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
           }
         }
-      if (ok && !leader && walk.last()) {
-        ok = wait_warp(&o_free, uint32_t(walk.item_no) & 1u, waits, 15);
-        if (ok && lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&o_free), 0));
-      }
     }
   } else {
     // ------------------------------------------------------------ softmax / epilogue
@@ -988,6 +978,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         m = mt;
       }
       const float mx = m == -INFINITY ? 0.f : m;
+      // P in registers, so that the scores' buffer is free for tile g + 2 before
+      // the value products of tile g - 1 have left P's
+      uint32_t pk[64];
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t r[32];
+        tmem_ld32(sc + 32 * w, r);
+        tmem_ld_wait();
+        reg_fence(r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scale_log2,
+                scale_log2, -mx, -mx);
+          x0 = fast_exp2(x0);
+          x1 = fast_exp2(x1);
+          fadd2(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], acc[2 * (i & 1)], acc[2 * (i & 1) + 1], x0,
+                x1);
+          pk[16 * w + i] = live ? pack_bf16x2(x0, x1) : 0u;  // (0: a pair's absent second node)
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_even(&s_free[g & 1]);
+      l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
       // O holds the products up to tile g - 1: rescale it once they are done.
       // Its halves of columns belong to different threads, all of one alpha
       // per row; alpha is 1 in an item's first tile.
@@ -1010,46 +1026,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       // The products of the first half of the keys add to all of O, so the
       // warps of the second half report their part of it before their own P.
       __syncwarp();
-      if (ok && half == 1 && lane == 0) mbar_arrive(&p_full[0]);
+      if (ok && half == 1 && lane == 0) arrive_even(&p_full[0]);
       // P goes to shared memory once the value products have read the last
       // tile's: for the first half of the keys in the middle of those products,
       // for the second half at their end, half of a tile's products before they
       // are needed.
       if (ok && g > 0) ok = wait_warp(&p_free[half], uint32_t(g - 1) & 1u, waits, 22);
       uint8_t* pr = smem + kOffP + half * 2 * kQBlk + row * 128;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int w = 0; w < 4; ++w) {
-        uint32_t r[32];
-        tmem_ld32(sc + 32 * w, r);
-        tmem_ld_wait();
-        reg_fence(r);
-        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x0, x1;
-          ffma2(x0, x1, __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scale_log2,
-                scale_log2, -mx, -mx);
-          x0 = fast_exp2(x0);
-          x1 = fast_exp2(x1);
-          fadd2(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], acc[2 * (i & 1)], acc[2 * (i & 1) + 1], x0,
-                x1);
-          pk[i] = live ? pack_bf16x2(x0, x1) : 0u;  // (P = 0 for a pair's absent second node)
-        }
-        uint8_t* pw = pr + (w >> 1) * kQBlk;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<uint4*>(pw + (((4 * (w & 1) + u) ^ (row & 7)) << 4)) =
-              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-      }
-      l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
-      tc_fence_before();
+      for (int u = 0; u < 16; ++u)
+        *reinterpret_cast<uint4*>(pr + (u >> 3) * kQBlk + (((u & 7) ^ (row & 7)) << 4)) =
+            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (ok && lane == 0) {
-        mbar_arrive(&s_free[g & 1]);
-        mbar_arrive(&p_full[half]);
-      }
+      if (ok && lane == 0) arrive_even(&p_full[half]);
       if (!walk.last()) continue;
 
       // ---- epilogue of the item
@@ -1097,7 +1087,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&o_free);
+      if (ok && lane == 0) arrive_even(&o_free);
     }
   }
 
@@ -1108,7 +1098,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   // Without an abort every block that was issued has been read by a product.
   const bool aborted =
       abort_flag != 0 || ld_shared_cluster_u32(mapa_shared(smem_u32(&abort_flag), rank ^ 1)) != 0;
-  if (aborted && warp == 9 && lane == 0) {
+  if (aborted && warp == 8 && lane == 0) {
     // cut blocks that were issued but not reported: they land on this CTA's
     // barriers, then count on the even CTA's
     int zero = 0;
