@@ -606,6 +606,8 @@ __device__ __forceinline__ uint32_t seen_keys(const AttnTreeArgs& a, const TreeR
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmC,
+                     const __grid_constant__ CUtensorMap tmO,
+                     const __grid_constant__ CUtensorMap tmPart,
                      const __grid_constant__ AttnTreeArgs a,
                      const __grid_constant__ Scratch s, float scale_log2,
                      unsigned long long wait_limit_ns, unsigned int* err_word, int test_stall) {
@@ -1032,6 +1034,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       // for the second half at their end, half of a tile's products before they
       // are needed.
       if (ok && g > 0) ok = wait_warp(&p_free[half], uint32_t(g - 1) & 1u, waits, 22);
+      if (g > 0 && walk.first()) {  // the last item's stores have read this memory
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        named_barrier_sync(1, 128);
+      }
       uint8_t* pr = smem + kOffP + half * 2 * kQBlk + row * 128;
 #pragma unroll
       for (int u = 0; u < 16; ++u)
@@ -1048,47 +1055,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       const float lsum = l + xsum[half ^ 1][row];
       ok = ok && wait_warp(&p_free[1], uint32_t(g) & 1u, waits, 23);
       tc_fence_after();
-      float* dst;
-      float f = 1.f;
-      if (walk.slot >= 0) {
-        const size_t prow = size_t(walk.slot) * 128 + rank * 64 + row;
-        if (half == 0 && live) s.part_ml[prow] = make_float2(m, lsum);
-        dst = s.part_o + prow * kLat;
-      } else {
-        f = lsum > 0.f ? 1.f / lsum : 0.f;
-        dst = s.o + (size_t(walk.it.r.start + node) * kHeads + row) * kLat;
-      }
-      // Row by row through shared memory (P's, free until the next tile's), so
-      // that a store instruction writes four whole 128-byte lines: a thread
-      // writing its own row took 10 thousand clocks an item.
-      float* base = dst - size_t(row) * kLat;
-      uint8_t* mine = smem + kOffP + (warp & 3) * 4096;  // [32 rows][128 bytes]
-      const int row0 = row & 32;                         // the warp's first row
+      // Each warp's 32 rows leave 32 columns at a time through shared memory (P's,
+      // free until the next tile's) as TMA stores, two in flight: a thread
+      // storing its own row took 10 thousand clocks an item, and O is free for
+      // the next item as soon as it is in registers.
+      const bool partial = walk.slot >= 0;
+      const float f = partial ? 1.f : (lsum > 0.f ? 1.f / lsum : 0.f);
+      const int row0 = row & 32;  // the warp's first row
+      const int to = partial ? walk.slot * 128 + int(rank) * 64 + row0
+                             : (walk.it.r.start + node) * kHeads + row0;
+      if (partial && half == 0 && live)
+        s.part_ml[size_t(walk.slot) * 128 + rank * 64 + row] = make_float2(m, lsum);
+      uint8_t* mine = smem + kOffP + (warp & 3) * 8192;  // 2 x [32 rows][128 bytes], swizzled
 #pragma unroll 1
       for (int c = 0; ok && live && c < 8; ++c) {
         uint32_t r[32];
         tmem_ld32(lanes + kColO + 32 * c, r);
         tmem_ld_wait();
         reg_fence(r);
+        uint8_t* at = mine + (c & 1) * 4096;
+        if (lane == 0) bulk_wait_group_read<1>();  // the store before last has read its buffer
+        __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          *reinterpret_cast<float4*>(mine + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+          *reinterpret_cast<float4*>(at + lane * 128 + ((u ^ (lane & 7)) << 4)) =
               make_float4(__uint_as_float(r[4 * u]) * f, __uint_as_float(r[4 * u + 1]) * f,
                           __uint_as_float(r[4 * u + 2]) * f, __uint_as_float(r[4 * u + 3]) * f);
+        fence_proxy_async_smem();
         __syncwarp();
-        float* to = base + (c >> 2) * 256 + half * 128 + (c & 3) * 32 + (lane & 7) * 4;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = 4 * k + (lane >> 3);
-          *reinterpret_cast<float4*>(to + size_t(row0 + rr) * kLat) =
-              *reinterpret_cast<const float4*>(mine + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+        if (lane == 0) {
+          const int col = ((c >> 2) * 256 + half * 128 + (c & 3) * 32) * 4;  // bytes
+          tma_store_2d(partial ? &tmPart : &tmO, at, col, to);
+          bulk_commit_group();
         }
-        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
       if (ok && lane == 0) arrive_even(&o_free);
     }
+    if (lane == 0) bulk_wait_group<0>();
   }
 
   // Teardown, first barrier: from here on neither CTA issues a copy.
@@ -1454,7 +1459,7 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   const Scratch s = carve(scratch, a.B, a.N);
   const int clusters = num_sms / 2 < kMaxClusters ? num_sms / 2 : kMaxClusters;
   const int box_rows = a.page_shift >= 6 ? 64 : 1 << a.page_shift;
-  CUtensorMap tmQ, tmC;
+  CUtensorMap tmQ, tmC, tmO, tmPart;
   const uint64_t q_dims[2] = {kRow, uint64_t(a.N) * kHeads};
   const uint64_t q_strides[1] = {kRow * 2};
   const uint32_t q_box[2] = {64, kHeads};
@@ -1463,6 +1468,14 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   const uint32_t c_box[3] = {64, uint32_t(box_rows), 1};
   if (!encode_tmap_bf16(&tmQ, s.q, 2, q_dims, q_strides, q_box, true) ||
       !encode_tmap_bf16(&tmC, a.cache, 3, c_dims, c_strides, c_box, true))
+    return cudaErrorInvalidValue;
+  // the results' rows of 512 floats, as bytes: boxes of 32 floats x 32 rows
+  const uint64_t o_dims[2] = {kLat * 4, uint64_t(a.N) * kHeads};
+  const uint64_t part_dims[2] = {kLat * 4, kMaxSlots * 128};
+  const uint64_t o_strides[1] = {kLat * 4};
+  const uint32_t o_box[2] = {128, 32};
+  if (!encode_tmap_u8(&tmO, s.o, 2, o_dims, o_strides, o_box, true) ||
+      !encode_tmap_u8(&tmPart, s.part_o, 2, part_dims, o_strides, o_box, true))
     return cudaErrorInvalidValue;
   const int tiles = (a.N + kQTok - 1) / kQTok;
   const dim3 qgrid(kHeads * 4, unsigned(tiles < 3 ? tiles : 3) + 1);
@@ -1477,8 +1490,8 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   static ContextCache attn_attr;
   e = ensure_smem_attr(reinterpret_cast<const void*>(tree_attn_kernel), int(kASmem), &attn_attr);
   if (e != cudaSuccess) return e;
-  e = launch_after(tree_attn_kernel, dim3(2 * clusters), kAThreads, kASmem, stream, tmQ, tmC, a, s,
-                   scale_log2, wait_limit_ns, err_word, test_stall);
+  e = launch_after(tree_attn_kernel, dim3(2 * clusters), kAThreads, kASmem, stream, tmQ, tmC, tmO,
+                   tmPart, a, s, scale_log2, wait_limit_ns, err_word, test_stall);
   if (e != cudaSuccess) return e;
   return a.N <= 2 * kVTok ? launch_value<64>(a, s, tiles, stream)
                           : launch_value<128>(a, s, tiles < 2 ? tiles : 2, stream);
