@@ -256,18 +256,19 @@ __device__ __forceinline__ void cp_wait() {
 }
 
 // ---------------------------------------------------------------- query
-// q~ = U_h^T q_nope: 16 tokens x 128 latent columns a step, contraction over
+// q~ = U_h^T q_nope: 32 tokens x 128 latent columns a step, contraction over
 // the head's 128 key dims. Grid (64 heads * 4 column quarters, y + 1): a CTA
 // keeps its 32 KB of weights in shared memory and walks every y-th token tile,
 // the next ones on their way. The CTAs of the first y row do the rest: the first
 // lays out the schedule and clears the status word, the others rotate the
 // rotary parts (a warp turns 8 heads of a token by one sine and cosine per
 // lane) and find the rows' requests.
-constexpr int kQTok = 16;
+constexpr int kQTok = 32;
 constexpr int kQThreads = 256;
 constexpr int kQCols = 128;
 constexpr int kQLd = 128 + 8;  // padded rows, in elements
 constexpr int kQHeads = 8;     // heads a warp rotates with one angle
+constexpr size_t kQSmem = size_t(kNope + 3 * kQTok) * kQLd * 2;
 
 template <bool kRope>
 __device__ void rotate_queries(const AttnTreeArgs& a, const Scratch& s, const RopeFreqs& f, int part,
@@ -324,18 +325,21 @@ __global__ void __launch_bounds__(kQThreads)
     }
     return;
   }
-  __shared__ __align__(16) __nv_bfloat16 sq[3][kQTok * kQLd];
-  __shared__ __align__(16) __nv_bfloat16 sw[kNope * kQLd];
+  extern __shared__ __align__(16) uint8_t smem[];
+  auto* sw = reinterpret_cast<__nv_bfloat16*>(smem);
+  auto* sq0 = sw + kNope * kQLd;  // [3][kQTok * kQLd]
   const int h = blockIdx.x >> 2, c0 = (blockIdx.x & 3) * kQCols;
   const int tiles = (a.N + kQTok - 1) / kQTok, step = gridDim.y - 1;
   const auto* qn = static_cast<const __nv_bfloat16*>(a.q_nope);
   const auto* w = static_cast<const __nv_bfloat16*>(a.w_kv_b) + size_t(h) * 256 * kLat + c0;
-  static_assert(kQTok * (kNope / 8) == kQThreads, "one piece of a query tile per thread");
   auto load = [&](int tile, int buf) {  // (a group of its own, empty past the last tile)
-    const int n = threadIdx.x / (kNope / 8), c = threadIdx.x % (kNope / 8) * 8;
-    const int row = min(tile * kQTok + n, a.N - 1);
     if (tile < tiles)
-      cp16(smem_u32(&sq[buf][n * kQLd + c]), qn + (size_t(row) * kHeads + h) * kNope + c, true);
+      for (int i = threadIdx.x; i < kQTok * (kNope / 8); i += kQThreads) {
+        const int n = i / (kNope / 8), c = i % (kNope / 8) * 8;
+        const int row = min(tile * kQTok + n, a.N - 1);
+        cp16(smem_u32(sq0 + (buf * kQTok + n) * kQLd + c),
+             qn + (size_t(row) * kHeads + h) * kNope + c, true);
+      }
     cp_commit();
   };
   for (int i = threadIdx.x; i < kNope * (kQCols / 8); i += kQThreads) {
@@ -347,36 +351,50 @@ __global__ void __launch_bounds__(kQThreads)
   load(first, 0);
   load(first + step, 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cw = warp * 16;  // this warp's 16 columns: two n-tiles
+  const int ct = warp % 2 * 16, cw = warp / 2 * 32;  // the warp's 16 tokens, 32 columns
   const int g = lane >> 2, t = lane & 3;
+  cp_wait<2>();
+  __syncthreads();
+  uint32_t fw[8][8];  // its weights, kept in registers: [step][n-tile pair]
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t r[4];
+      ldsm4t(r, smem_u32(sw + (k * 16 + (lane & 15)) * kQLd + cw + i * 16 + (lane >> 4) * 8));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) fw[k][4 * i + q] = r[q];
+    }
   int buf = 0;
   for (int tile = first; tile < tiles; tile += step, buf = buf == 2 ? 0 : buf + 1) {
     // two tiles ahead, into the buffer the tile before this one left
     load(tile + 2 * step, buf == 0 ? 2 : buf - 1);
     cp_wait<2>();
     __syncthreads();
-    float d[2][4] = {};
+    __nv_bfloat16* sq = sq0 + buf * kQTok * kQLd;
+    float d[4][4] = {};
 #pragma unroll
     for (int k = 0; k < kNope / 16; ++k) {
-      uint32_t fa[4], fb[4];
-      ldsm4(fa, smem_u32(&sq[buf][(lane & 15) * kQLd + k * 16 + (lane >> 4) * 8]));
-      ldsm4t(fb, smem_u32(sw + (k * 16 + (lane & 15)) * kQLd + cw + (lane >> 4) * 8));
-      mma_16816(d[0], fa, fb[0], fb[1]);
-      mma_16816(d[1], fa, fb[2], fb[3]);
+      uint32_t fa[4];
+      ldsm4(fa, smem_u32(sq + (ct + (lane & 15)) * kQLd + k * 16 + (lane >> 4) * 8));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mma_16816(d[i], fa, fw[k][2 * i], fw[k][2 * i + 1]);
     }
     // through the query tile's own buffer, so that a row leaves in whole lines
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int half = 0; half < 2; ++half)
-        *reinterpret_cast<uint32_t*>(&sq[buf][(g + 8 * half) * kQLd + cw + 8 * j + 2 * t]) =
-            pack_bf16x2(d[j][2 * half], d[j][2 * half + 1]);
+        *reinterpret_cast<uint32_t*>(sq + (ct + g + 8 * half) * kQLd + cw + 8 * i + 2 * t) =
+            pack_bf16x2(d[i][2 * half], d[i][2 * half + 1]);
     __syncthreads();
-    const int n = tile * kQTok + threadIdx.x / 16, c = threadIdx.x % 16 * 8;
-    if (n < a.N)
-      *reinterpret_cast<uint4*>(s.q + (size_t(n) * kHeads + h) * kRow + c0 + c) =
-          *reinterpret_cast<const uint4*>(&sq[buf][(threadIdx.x / 16) * kQLd + c]);
+    for (int i = threadIdx.x; i < kQTok * (kQCols / 8); i += kQThreads) {
+      const int n = i / (kQCols / 8), c = i % (kQCols / 8) * 8;
+      if (tile * kQTok + n < a.N)
+        *reinterpret_cast<uint4*>(s.q + (size_t(tile * kQTok + n) * kHeads + h) * kRow + c0 + c) =
+            *reinterpret_cast<const uint4*>(sq + n * kQLd + c);
+    }
     __syncthreads();  // the buffer is loaded again
   }
 }
@@ -1477,13 +1495,19 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   if (!encode_tmap_u8(&tmO, s.o, 2, o_dims, o_strides, o_box, true) ||
       !encode_tmap_u8(&tmPart, s.part_o, 2, part_dims, o_strides, o_box, true))
     return cudaErrorInvalidValue;
-  const int tiles = (a.N + kQTok - 1) / kQTok;
-  const dim3 qgrid(kHeads * 4, unsigned(tiles < 3 ? tiles : 3) + 1);
-  if (rotary)
-    tree_query_kernel<true><<<qgrid, kQThreads, 0, stream>>>(a, s, *rotary, clusters, err_word);
-  else
-    tree_query_kernel<false><<<qgrid, kQThreads, 0, stream>>>(a, s, RopeFreqs{}, clusters, err_word);
-  cudaError_t e = cudaGetLastError();
+  // One CTA per head and column quarter walks all tokens up to 256 of them, up
+  // to four share them beyond (three CTAs fit an SM: 256 tokens in one wave).
+  const int q_tiles = (a.N + kQTok - 1) / kQTok;
+  const int y = q_tiles <= 8 ? 1 : q_tiles <= 32 ? (q_tiles + 7) / 8 : 4;
+  const dim3 qgrid(kHeads * 4, unsigned(y) + 1);
+  static ContextCache query_attr[2];
+  auto query = rotary ? tree_query_kernel<true> : tree_query_kernel<false>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(query), int(kQSmem),
+                                   &query_attr[rotary ? 1 : 0]);
+  if (e != cudaSuccess) return e;
+  query<<<qgrid, kQThreads, kQSmem, stream>>>(a, s, rotary ? *rotary : RopeFreqs{}, clusters,
+                                             err_word);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   float scale_log2 = a.scale * 1.4426950408889634f;
   if (scale_log2 == 0.f) scale_log2 = std::numeric_limits<float>::min();  // see `hidden`
@@ -1493,6 +1517,7 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   e = launch_after(tree_attn_kernel, dim3(2 * clusters), kAThreads, kASmem, stream, tmQ, tmC, tmO,
                    tmPart, a, s, scale_log2, wait_limit_ns, err_word, test_stall);
   if (e != cudaSuccess) return e;
+  const int tiles = (a.N + kVTok - 1) / kVTok;
   return a.N <= 2 * kVTok ? launch_value<64>(a, s, tiles, stream)
                           : launch_value<128>(a, s, tiles < 2 ? tiles : 2, stream);
 }
