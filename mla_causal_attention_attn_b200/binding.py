@@ -583,9 +583,18 @@ PAGE_SIZES = (16, 32, 64, 128)
 W4_GROUPS = (32, 64, 128)
 
 
+# A step's calls are short, so their checks are too: one comparison per property,
+# the message worked out only when one fails.
+
+
 @contextlib.contextmanager
-def _entered(dev, stream):
-    with torch.cuda.device(dev):
+def _launching(index, stream):
+    """Device ``index`` current, and ``stream`` too when one is given, so that
+    what the call allocates belongs to the stream its kernels use. Yields the
+    stream handle."""
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    with torch.cuda.device(index):
         if stream is None:
             yield int(torch.cuda.current_stream().cuda_stream)
         else:
@@ -593,46 +602,38 @@ def _entered(dev, stream):
                 yield int(stream.cuda_stream)
 
 
-class _Here:
-    """The usual call: tensors on the current device, its current stream."""
-
-    def __enter__(self):
-        return int(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        return False
+# torch's own bindings of the two queries: torch.cuda.current_stream() builds a
+# Stream object, 3.3 us a call against 0.1.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-_HERE = _Here()
+def _run(index, stream, call):
+    """``call(stream handle)`` on device ``index`` and ``stream`` (None: its
+    current one)."""
+    if stream is None and _raw_stream and _current_device and _current_device() == index:
+        return call(_raw_stream(index))
+    with _launching(index, stream) as handle:
+        return call(handle)
 
 
-def _launching(dev, stream):
-    """Context in which a call on ``dev``'s tensors runs: that device current,
-    and ``stream`` too when one is given, so that what the call allocates
-    belongs to the stream its kernels use. Yields the stream handle."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    if stream is None and dev.index == torch.cuda.current_device():
-        return _HERE
-    return _entered(dev, stream)
-
-
-def _on(dev, t, dtype, shape, name):
-    """_req_t, and the tensor lies on ``dev``."""
-    if t.dtype != dtype:
+def _on(index, t, dtype, shape, name):
+    """A contiguous ``dtype`` tensor of ``shape`` on CUDA device ``index``."""
+    if (t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
+        return
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _cuda_device(t, name):
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
 def _cache_pages(cache, dev):
@@ -640,8 +641,8 @@ def _cache_pages(cache, dev):
     cache whose rows are dense (the pages may lie apart)."""
     if cache.dtype != torch.bfloat16:
         raise TypeError(f"cache must be bf16, got {cache.dtype}")
-    if cache.device != dev:
-        raise ValueError(f"cache must be on {dev}, got {cache.device}")
+    if cache.get_device() != dev:
+        raise ValueError(f"cache must be on cuda:{dev}, got {cache.device}")
     if cache.dim() != 3 or cache.shape[2] != CACHE_DIM:
         raise ValueError(f"cache must be [pages, page_size, {CACHE_DIM}], got {tuple(cache.shape)}")
     n, page, _ = cache.shape
@@ -659,7 +660,7 @@ def page_plan(context_len, new_len, free_pages, block_table, page_size, num_page
     (cu_new [B+1], slot_map [max_tokens], positions [max_tokens], counts [2]),
     all int32 (``out`` gives them), and writes the new pages' entries into
     ``block_table`` [B, max_pages]."""
-    lib = load()
+    lib = _lib or load()
     dev = _cuda_device(context_len, "context_len")
     i32 = torch.int32
     B = context_len.shape[0]
@@ -672,22 +673,34 @@ def page_plan(context_len, new_len, free_pages, block_table, page_size, num_page
     _on(dev, block_table, i32, (B, cols), "block_table")
     if node_depth is not None:
         _on(dev, node_depth, i32, (max_tokens,), "node_depth")
-    with _launching(dev, stream) as handle:
-        if out is None:
-            out = tuple(torch.empty(n, dtype=i32, device=dev)
+    if out is not None:
+        _plan_out(dev, out, B, max_tokens)
+
+    def call(handle):
+        res = out
+        if res is None:
+            res = tuple(torch.empty(n, dtype=i32, device=context_len.device)
                         for n in (B + 1, max_tokens, max_tokens, 2))
-        cu, slots, pos, counts = out
-        _on(dev, cu, i32, (B + 1,), "cu_new")
-        _on(dev, slots, i32, (max_tokens,), "slot_map")
-        _on(dev, pos, i32, (max_tokens,), "positions")
-        _on(dev, counts, i32, (2,), "counts")
+        cu, slots, pos, counts = res
         st = lib.mla_page_plan(context_len.data_ptr(), new_len.data_ptr(), B,
                                free_pages.data_ptr() if n_free else None, n_free,
-                               _ptr(node_depth), num_pages, page_size, block_table.data_ptr(),
-                               cols, cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), max_tokens,
+                               node_depth.data_ptr() if node_depth is not None else None,
+                               num_pages, page_size, block_table.data_ptr(), cols,
+                               cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), max_tokens,
                                counts.data_ptr(), handle)
-    _check("mla_page_plan", st)
-    return out
+        if st:
+            _check("mla_page_plan", st)
+        return res
+
+    return _run(dev, stream, call)
+
+
+def _plan_out(dev, out, B, max_tokens):
+    cu, slots, pos, counts = out
+    _on(dev, cu, torch.int32, (B + 1,), "cu_new")
+    _on(dev, slots, torch.int32, (max_tokens,), "slot_map")
+    _on(dev, pos, torch.int32, (max_tokens,), "positions")
+    _on(dev, counts, torch.int32, (2,), "counts")
 
 
 def cache_append(c_kv, k_pe, slot_map, cache, positions=None, rope=None, stream=None):
@@ -695,7 +708,7 @@ def cache_append(c_kv, k_pe, slot_map, cache, positions=None, rope=None, stream=
     [pages, page_size, 576] via ``mla_cache_append``; ``rope`` (a mapping of
     config.json's rotary fields) rotates k_pe at ``positions`` [N], None stores
     it as it is. Returns ``cache``."""
-    lib = load()
+    lib = _lib or load()
     dev = _cuda_device(c_kv, "c_kv")
     N = c_kv.shape[0]
     _on(dev, c_kv, torch.bfloat16, (N, KV_RANK), "c_kv")
@@ -703,13 +716,16 @@ def cache_append(c_kv, k_pe, slot_map, cache, positions=None, rope=None, stream=
     _on(dev, slot_map, torch.int32, (N,), "slot_map")
     n_pages, page, stride = _cache_pages(cache, dev)
     yr = _step_rope(rope, positions, N, dev)
-    with _launching(dev, stream) as handle:
-        st = lib.mla_cache_append(c_kv.data_ptr(), k_pe.data_ptr(),
-                                  positions.data_ptr() if yr is not None else None, yr,
-                                  slot_map.data_ptr(), N, cache.data_ptr(), n_pages, page, stride,
-                                  handle)
-    _check("mla_cache_append", st)
-    return cache
+
+    def call(handle):
+        _check("mla_cache_append",
+               lib.mla_cache_append(c_kv.data_ptr(), k_pe.data_ptr(),
+                                    positions.data_ptr() if yr is not None else None, yr,
+                                    slot_map.data_ptr(), N, cache.data_ptr(), n_pages, page,
+                                    stride, handle))
+        return cache
+
+    return _run(dev, stream, call)
 
 
 def _step_rope(rope, positions, N, dev):
@@ -732,7 +748,7 @@ def attn_tree(q_nope, q_pe, W_kv_b, cache, block_table, context_len, cu_new, tre
     over the paged cache, merged heads [N, 8192] bf16, via ``mla_attn_tree``.
     ``tree_mask`` [N, words] int32 holds the visible nodes' bits (None: a
     chain); ``rope`` rotates q_pe at ``positions`` (None: rotated already)."""
-    lib = load()
+    lib = _lib or load()
     dev = _cuda_device(q_nope, "q_nope")
     bf16, i32 = torch.bfloat16, torch.int32
     N, B = q_nope.shape[0], context_len.shape[0]
@@ -750,48 +766,62 @@ def attn_tree(q_nope, q_pe, W_kv_b, cache, block_table, context_len, cu_new, tre
         _on(dev, tree_mask, i32, (N, words), "tree_mask")
     yr = _step_rope(rope, positions, N, dev)
     scale = _inputs.DEFAULT_SCALE if softmax_scale is None else float(softmax_scale)
-    with _launching(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((N, K_OPROJ), dtype=bf16, device=dev)
-        if workspace is None:
-            workspace = torch.empty(attn_tree_workspace_bytes(B, N), dtype=torch.uint8, device=dev)
+    if out is not None:
         _on(dev, out, bf16, (N, K_OPROJ), "out")
-        st = lib.mla_attn_tree(q_nope.data_ptr(), q_pe.data_ptr(), W_kv_b.data_ptr(),
-                               positions.data_ptr() if yr is not None else None, yr,
-                               cache.data_ptr(), n_pages, page, stride, block_table.data_ptr(),
-                               cols, context_len.data_ptr(), cu_new.data_ptr(), _ptr(tree_mask),
-                               words, B, N, scale, workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), out.data_ptr(),
-                               handle)
-    _check("mla_attn_tree", st)
-    return out
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous, on cuda:{dev}")
+
+    def call(handle):
+        o, ws = out, workspace
+        if o is None:
+            o = torch.empty((N, K_OPROJ), dtype=bf16, device=q_nope.device)
+        if ws is None:
+            ws = torch.empty(attn_tree_workspace_bytes(B, N), dtype=torch.uint8,
+                             device=q_nope.device)
+        _check("mla_attn_tree",
+               lib.mla_attn_tree(q_nope.data_ptr(), q_pe.data_ptr(), W_kv_b.data_ptr(),
+                                 positions.data_ptr() if yr is not None else None, yr,
+                                 cache.data_ptr(), n_pages, page, stride, block_table.data_ptr(),
+                                 cols, context_len.data_ptr(), cu_new.data_ptr(),
+                                 tree_mask.data_ptr() if tree_mask is not None else None, words,
+                                 B, N, scale, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                 o.data_ptr(), handle))
+        return o
+
+    return _run(dev, stream, call)
 
 
 def quantize_weight_w4(W_o, group=128, q=None, scale=None, stream=None):
     """4-bit codes [7168, 4096] (uint8, two a byte) and group scales
     [7168, 8192 / group] (bf16) of ``W_o`` via ``mla_quantize_weight_w4``."""
-    lib = load()
+    lib = _lib or load()
     dev = _cuda_device(W_o, "W_o")
     if group not in W4_GROUPS:
         raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
     _on(dev, W_o, torch.bfloat16, (D_MODEL, K_OPROJ), "W_o")
-    with _launching(dev, stream) as handle:
-        if q is None:
-            q = torch.empty((D_MODEL, K_OPROJ // 2), dtype=torch.uint8, device=dev)
-        if scale is None:
-            scale = torch.empty((D_MODEL, K_OPROJ // group), dtype=torch.bfloat16, device=dev)
+    if q is not None:
         _on(dev, q, torch.uint8, (D_MODEL, K_OPROJ // 2), "q")
+    if scale is not None:
         _on(dev, scale, torch.bfloat16, (D_MODEL, K_OPROJ // group), "scale")
-        st = lib.mla_quantize_weight_w4(W_o.data_ptr(), group, q.data_ptr(), scale.data_ptr(),
-                                        handle)
-    _check("mla_quantize_weight_w4", st)
-    return q, scale
+
+    def call(handle):
+        c, sc = q, scale
+        if c is None:
+            c = torch.empty((D_MODEL, K_OPROJ // 2), dtype=torch.uint8, device=W_o.device)
+        if sc is None:
+            sc = torch.empty((D_MODEL, K_OPROJ // group), dtype=torch.bfloat16, device=W_o.device)
+        _check("mla_quantize_weight_w4",
+               lib.mla_quantize_weight_w4(W_o.data_ptr(), group, c.data_ptr(), sc.data_ptr(),
+                                          handle))
+        return c, sc
+
+    return _run(dev, stream, call)
 
 
 def o_proj_w4(attn, W_q, W_scale, out=None, stream=None):
     """o_proj with 4-bit weights -> [M, 7168] bf16 via ``mla_o_proj_w4``; the
     group size is 8192 / W_scale's columns."""
-    lib = load()
+    lib = _lib or load()
     dev = _cuda_device(attn, "attn")
     M = attn.shape[0]
     _on(dev, attn, torch.bfloat16, (M, K_OPROJ), "attn")
@@ -800,14 +830,20 @@ def o_proj_w4(attn, W_q, W_scale, out=None, stream=None):
     if groups not in (64, 128, 256):
         raise ValueError(f"W_scale must have 64, 128 or 256 columns, got {groups}")
     _on(dev, W_scale, torch.bfloat16, (D_MODEL, groups), "W_scale")
-    with _launching(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((M, D_MODEL), dtype=torch.bfloat16, device=dev)
+    if out is not None:
         _on(dev, out, torch.bfloat16, (M, D_MODEL), "out")
+
+    def call(handle):
+        o = out
+        if o is None:
+            o = torch.empty((M, D_MODEL), dtype=torch.bfloat16, device=attn.device)
         st = lib.mla_o_proj_w4(attn.data_ptr(), W_q.data_ptr(), W_scale.data_ptr(),
-                               K_OPROJ // groups, M, out.data_ptr(), handle)
-    _check("mla_o_proj_w4", st)
-    return out
+                               K_OPROJ // groups, M, o.data_ptr(), handle)
+        if st:
+            _check("mla_o_proj_w4", st)
+        return o
+
+    return _run(dev, stream, call)
 
 
 def device_status(stream=None):
