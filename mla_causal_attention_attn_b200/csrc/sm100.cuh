@@ -28,6 +28,7 @@ enum : unsigned int {
   kErrKernelOprojSmallM = 4u << 8,
   kErrKernelOprojFp8 = 5u << 8,
   kErrKernelTree = 6u << 8,
+  kErrKernelOprojW4 = 7u << 8,
   kErrTimeoutFlag = 1u << 16,
 };
 

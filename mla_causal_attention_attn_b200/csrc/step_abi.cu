@@ -167,7 +167,10 @@ mla_status_t mla_o_proj_w4(const mla_bf16* attn, const uint8_t* W_q, const mla_b
     return MLA_ERR_MISALIGNED;
   mla_status_t s = check_device();
   if (s != MLA_OK) return s;
+  unsigned int* err = device_error_word();
+  if (!err) return MLA_ERR_CUDA;
   return from_cuda(launch_oproj_w4(attn, W_q, W_scale, group, out, M, MLA_HIDDEN, MLA_OPROJ_IN,
+                                   wait_limit_ns(), err, test_stall_wait() == 2 ? 1 : 0,
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 

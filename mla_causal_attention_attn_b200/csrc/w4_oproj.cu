@@ -127,42 +127,38 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
 
 constexpr int kW4Threads = 256;
 constexpr int kW4Warps = 8;
+constexpr int kW4Rows = 16;
+constexpr int kW4Tokens = 8;
 constexpr int kW4Step = 128;      // features of a step
 constexpr int kW4Ring = 4;        // steps on their way
 constexpr int kW4Pitch = kW4Step / 2 * kW4Ring + 16;  // bytes of a row in the ring: 8 rows x 4 words
                                                       // hit 32 banks
-template <int RT>
-constexpr int w4_smem() { return kW4Warps * 16 * RT * kW4Pitch; }
-template <int NT, int RT>
-constexpr bool kWarpsFit = kW4Warps * 8 * NT * (16 * RT + 1) * 4 <= w4_smem<RT>();
 
-// A CTA computes 16 RT weight rows times 8 NT tokens; its 8 warps take 1024
+// A CTA computes 16 weight rows times up to 8 tokens; its 8 warps take 1024
 // features each, 128 a step. A warp streams its codes through a ring of its own
 // in shared memory (four steps ahead, cp.async), the tokens' features come
 // straight from L1 and L2. Lane (row g = lane / 4, quarter t = lane % 4) takes
-// the word of 8 features 32 w + 8 t .. + 7 of rows g and g + 8 of a 16-row tile
-// and of token g; the word gives the pairs (j, j + 4), j = 0..3, for both
-// operands, and 32 features never cross a group. Sums of a group are scaled in
-// fp32, the warps' sums meet in shared memory in a fixed order.
-template <int NT, int RT, int kGroup>
+// the word of 8 features 32 w + 8 t .. + 7 of rows g and g + 8 and of token g;
+// the word gives the pairs (j, j + 4), j = 0..3, for both operands, and 32
+// features never cross a group. Sums of a group are scaled in fp32, the warps'
+// sums meet in shared memory in a fixed order.
+template <int kGroup>
 __global__ void __launch_bounds__(kW4Threads)
     oproj_w4_kernel(const __nv_bfloat16* __restrict__ A, const uint8_t* __restrict__ q,
-                    const __nv_bfloat16* __restrict__ scale, __nv_bfloat16* __restrict__ C,
-                    int64_t M, int N, int K) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kRows = 16 * RT;
+                    const __nv_bfloat16* __restrict__ scale, __nv_bfloat16* __restrict__ C, int M,
+                    int N, int K) {
+  __shared__ __align__(16) uint8_t smem[kW4Warps * kW4Rows * kW4Pitch];
   constexpr int kPer = kW4Step / kGroup;  // groups of a step
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int n0 = int(blockIdx.x) * kRows;
+  const int n0 = int(blockIdx.x) * kW4Rows;
   const int slice = K / kW4Warps, k0 = warp * slice, steps = slice / kW4Step;
-  const int64_t m0 = int64_t(blockIdx.y) * (8 * NT);
-  uint8_t* ring = smem + warp * kRows * kW4Pitch;
+  uint8_t* ring = smem + warp * kW4Rows * kW4Pitch;
   const uint8_t* q0 = q + size_t(n0) * (K / 2) + k0 / 2;
   auto fetch = [&](int step) {  // one group of copies, empty past the last step
     if (step < steps)
 #pragma unroll
-      for (int i = 0; i < 2 * RT; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const int c = i * 32 + lane, row = c >> 2, piece = c & 3;
         cp16(smem_u32(ring + row * kW4Pitch + (step % kW4Ring) * 64 + piece * 16),
              q0 + size_t(row) * (K / 2) + step * 64 + piece * 16);
@@ -173,149 +169,514 @@ __global__ void __launch_bounds__(kW4Threads)
   for (int i = 0; i < kW4Ring; ++i) fetch(i);
 
   // (tokens past M repeat the last one; their sums are not stored)
-  const __nv_bfloat16* xp[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int64_t m = m0 + 8 * i + g;
-    xp[i] = A + (m < M ? m : M - 1) * K + k0 + 8 * t;
-  }
+  const __nv_bfloat16* xp = A + size_t(g < M ? g : M - 1) * K + k0 + 8 * t;
   const __nv_bfloat16* sp = scale + size_t(n0 + g) * (K / kGroup) + k0 / kGroup;
-  float acc[RT][NT][4] = {};
-  // the step's tokens and scales, loaded a step ahead where registers allow
-  constexpr int kBuf = NT * RT <= 4 ? 2 : 1;
-  uint4 xs[kBuf][4][NT];
-  uint32_t ss[kBuf][RT][2][(kPer + 1) / 2];
+  float acc[4] = {};
+  // the step's tokens and scales, loaded a step ahead
+  uint4 xs[2][4];
+  uint32_t ss[2][2][(kPer + 1) / 2];
   auto operands = [&](int step, int b) {
     if (step >= steps) return;
 #pragma unroll
     for (int w = 0; w < 4; ++w)
+      xs[b][w] = __ldg(reinterpret_cast<const uint4*>(xp + step * kW4Step + w * 32));
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        xs[b][w][i] = __ldg(reinterpret_cast<const uint4*>(xp[i] + step * kW4Step + w * 32));
+    for (int h = 0; h < 2; ++h) {
+      const __nv_bfloat16* p = sp + size_t(h * 8) * (K / kGroup) + step * kPer;
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const __nv_bfloat16* p = sp + size_t(r * 16 + h * 8) * (K / kGroup) + step * kPer;
-#pragma unroll
-        for (int e = 0; e < (kPer + 1) / 2; ++e)
-          ss[b][r][h][e] = kPer == 1 ? *reinterpret_cast<const uint16_t*>(p)
-                                     : reinterpret_cast<const uint32_t*>(p)[e];
-      }
+      for (int e = 0; e < (kPer + 1) / 2; ++e)
+        ss[b][h][e] = kPer == 1 ? *reinterpret_cast<const uint16_t*>(p)
+                                : reinterpret_cast<const uint32_t*>(p)[e];
+    }
   };
   operands(0, 0);
   auto one_step = [&](int step, int b) {
-    if (kBuf == 2) operands(step + 1, b ^ 1);
-    const uint4(&x)[4][NT] = xs[b];
-    float s[RT][2][kPer];
+    operands(step + 1, b ^ 1);
+    const uint4(&x)[4] = xs[b];
+    float s[2][kPer];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          s[r][h][e] = __uint_as_float(e & 1 ? ss[b][r][h][e / 2] & 0xffff0000u : ss[b][r][h][e / 2] << 16);
+      for (int e = 0; e < kPer; ++e)
+        s[h][e] = __uint_as_float(e & 1 ? ss[b][h][e / 2] & 0xffff0000u : ss[b][h][e / 2] << 16);
     asm volatile("cp.async.wait_group %0;" ::"n"(kW4Ring - 1) : "memory");
     __syncwarp();
     const uint8_t* cw = ring + g * kW4Pitch + (step % kW4Ring) * 64 + t * 4;
-    float d[RT][NT][4];
+    float d[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      uint32_t xb[NT][4];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        xb[i][0] = __byte_perm(x[w][i].x, x[w][i].z, 0x5410);
-        xb[i][1] = __byte_perm(x[w][i].x, x[w][i].z, 0x7632);
-        xb[i][2] = __byte_perm(x[w][i].y, x[w][i].w, 0x5410);
-        xb[i][3] = __byte_perm(x[w][i].y, x[w][i].w, 0x7632);
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const uint32_t a0 = *reinterpret_cast<const uint32_t*>(cw + (r * 16) * kW4Pitch + w * 16);
-        const uint32_t a1 = *reinterpret_cast<const uint32_t*>(cw + (r * 16 + 8) * kW4Pitch + w * 16);
-        const uint32_t f0[4] = {codes_to_bf16x2(a0), codes_to_bf16x2(a1),
-                                codes_to_bf16x2(a0 >> 4),
-                                codes_to_bf16x2(a1 >> 4)};
-        const uint32_t f1[4] = {codes_to_bf16x2(a0 >> 8),
-                                codes_to_bf16x2(a1 >> 8),
-                                codes_to_bf16x2(a0 >> 12),
-                                codes_to_bf16x2(a1 >> 12)};
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          if (w * 32 % kGroup == 0)
-            mma_16816_first(d[r][i], f0, xb[i][0], xb[i][1]);
-          else
-            mma_16816(d[r][i], f0, xb[i][0], xb[i][1]);
-          mma_16816(d[r][i], f1, xb[i][2], xb[i][3]);
-        }
-        if ((w + 1) * 32 % kGroup == 0) {
-          const float s0 = s[r][0][w * 32 / kGroup], s1 = s[r][1][w * 32 / kGroup];
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            acc[r][i][0] = fmaf(d[r][i][0], s0, acc[r][i][0]);
-            acc[r][i][1] = fmaf(d[r][i][1], s0, acc[r][i][1]);
-            acc[r][i][2] = fmaf(d[r][i][2], s1, acc[r][i][2]);
-            acc[r][i][3] = fmaf(d[r][i][3], s1, acc[r][i][3]);
-          }
-        }
+      const uint32_t xb[4] = {
+          __byte_perm(x[w].x, x[w].z, 0x5410), __byte_perm(x[w].x, x[w].z, 0x7632),
+          __byte_perm(x[w].y, x[w].w, 0x5410), __byte_perm(x[w].y, x[w].w, 0x7632)};
+      const uint32_t a0 = *reinterpret_cast<const uint32_t*>(cw + w * 16);
+      const uint32_t a1 = *reinterpret_cast<const uint32_t*>(cw + 8 * kW4Pitch + w * 16);
+      const uint32_t f0[4] = {codes_to_bf16x2(a0), codes_to_bf16x2(a1), codes_to_bf16x2(a0 >> 4),
+                              codes_to_bf16x2(a1 >> 4)};
+      const uint32_t f1[4] = {codes_to_bf16x2(a0 >> 8), codes_to_bf16x2(a1 >> 8),
+                              codes_to_bf16x2(a0 >> 12), codes_to_bf16x2(a1 >> 12)};
+      if (w * 32 % kGroup == 0)
+        mma_16816_first(d, f0, xb[0], xb[1]);
+      else
+        mma_16816(d, f0, xb[0], xb[1]);
+      mma_16816(d, f1, xb[2], xb[3]);
+      if ((w + 1) * 32 % kGroup == 0) {
+        const float s0 = s[0][w * 32 / kGroup], s1 = s[1][w * 32 / kGroup];
+        acc[0] = fmaf(d[0], s0, acc[0]);
+        acc[1] = fmaf(d[1], s0, acc[1]);
+        acc[2] = fmaf(d[2], s1, acc[2]);
+        acc[3] = fmaf(d[3], s1, acc[3]);
       }
     }
     __syncwarp();
     fetch(step + kW4Ring);
-    if (kBuf == 1) operands(step + 1, 0);
   };
 #pragma unroll 1
   for (int step = 0; step < steps; step += 2) {  // (K % 2048 == 0)
     one_step(step, 0);
-    one_step(step + 1, kBuf - 1);
+    one_step(step + 1, 1);
   }
   // the warps' sums, [warp][token][row], in the ring's memory
-  constexpr int kTok = 8 * NT, kLd = kRows + 1;
-  static_assert(kWarpsFit<NT, RT>, "the sums fit");
+  constexpr int kLd = kW4Rows + 1;
+  static_assert(kW4Warps * kW4Tokens * kLd * 4 <= sizeof(smem), "the sums fit");
   float* red = reinterpret_cast<float*>(smem);
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        red[(warp * kTok + 8 * i + 2 * t + (e & 1)) * kLd + r * 16 + g + (e >> 1) * 8] = acc[r][i][e];
+  for (int e = 0; e < 4; ++e)
+    red[(warp * kW4Tokens + 2 * t + (e & 1)) * kLd + g + (e >> 1) * 8] = acc[e];
   __syncthreads();
-  for (int i = tid; i < kTok * kRows; i += kW4Threads) {
-    const int tok = i / kRows, row = i % kRows;
+  if (tid < kW4Tokens * kW4Rows) {
+    const int tok = tid / kW4Rows, row = tid % kW4Rows;
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kW4Warps; ++w) sum += red[(w * kTok + tok) * kLd + row];
-    if (m0 + tok < M) C[(m0 + tok) * N + n0 + row] = __float2bfloat16_rn(sum);
+    for (int w = 0; w < kW4Warps; ++w) sum += red[(w * kW4Tokens + tok) * kLd + row];
+    if (tok < M) C[size_t(tok) * N + n0 + row] = __float2bfloat16_rn(sum);
   }
-}
-
-template <int NT, int RT, int kGroup>
-cudaError_t launch_nt(const void* A, const void* q, const void* scale, void* C, int64_t M, int N,
-                      int K, cudaStream_t stream) {
-  auto kern = oproj_w4_kernel<NT, RT, kGroup>;
-  static ContextCache attr;
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), w4_smem<RT>(), &attr);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(unsigned(N / (16 * RT)), unsigned((M + 8 * NT - 1) / (8 * NT)));
-  kern<<<grid, kW4Threads, w4_smem<RT>(), stream>>>(
-      static_cast<const __nv_bfloat16*>(A), static_cast<const uint8_t*>(q),
-      static_cast<const __nv_bfloat16*>(scale), static_cast<__nv_bfloat16*>(C), M, N, K);
-  return cudaGetLastError();
 }
 
 template <int kGroup>
-cudaError_t launch_group(const void* A, const void* q, const void* scale, void* C, int64_t M, int N,
-                         int K, cudaStream_t stream) {
-  if (M <= 8) return launch_nt<1, 1, kGroup>(A, q, scale, C, M, N, K, stream);
-  if (M <= 16) return launch_nt<2, 2, kGroup>(A, q, scale, C, M, N, K, stream);
-  const int64_t passes = (M + 39) / 40;
-  switch ((M + 8 * passes - 1) / (8 * passes)) {
-    case 3: return launch_nt<3, 4, kGroup>(A, q, scale, C, M, N, K, stream);
-    case 4: return launch_nt<4, 4, kGroup>(A, q, scale, C, M, N, K, stream);
-    default: return launch_nt<5, 4, kGroup>(A, q, scale, C, M, N, K, stream);
+cudaError_t launch_stream(const void* A, const void* q, const void* scale, void* C, int64_t M,
+                          int N, int K, cudaStream_t stream) {
+  oproj_w4_kernel<kGroup><<<N / kW4Rows, kW4Threads, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(A), static_cast<const uint8_t*>(q),
+      static_cast<const __nv_bfloat16*>(scale), static_cast<__nv_bfloat16*>(C), int(M), N, K);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- product, more rows
+// D = W_tile . x^T on the tensor cores: 128 weight rows (the MMA's M) times NT
+// tokens (its N), the two CTAs of a cluster take half of K each. Codes arrive by
+// TMA (128 rows x 256 features, 16 KB, kStages on their way); eight warps turn
+// them into bf16 integers -8 .. 7 (exact) and write them to tensor memory as the
+// A operand, 128 features a step; x arrives by TMA as the B operand. The MMAs of
+// a scale group write a fresh fp32 sum, which eight more warps read back,
+// multiply by the row's scale and add into fp32 registers, so nothing is rounded
+// before the final bf16. A unit is what those warps take at once: two groups of
+// 32 or 64 features, one of 128; even units go to the first four warps, odd ones
+// to the others. The four partial sums meet in shared memory, the cluster's
+// included, in a fixed order.
+constexpr int kTcThreads = 640;  // 8 warps unpack, 8 scale and add, 2 issue MMAs, 1 loads
+// 640 threads get 96 registers each; the warpgroups share them out:
+// 2 x 128 x 80 + 2 x 128 x 136 + 128 x 48 = 640 x 96.
+constexpr uint32_t kRegsUnpack = 80, kRegsAdd = 136, kRegsIssue = 48;
+constexpr int kIssuers = 2;
+constexpr int kTcRows = 128;
+
+template <int NT, int kGroup>
+struct TcCfg {
+  static constexpr int kStages = 5;                  // 256 features of codes
+  static constexpr int kSteps = 4;                   // 128 features of x and unpacked codes
+  static constexpr uint32_t kCodeBytes = kTcRows * 128;
+  static constexpr uint32_t kXHalf = NT * 128;       // 64 features of the tokens
+  static constexpr int kUnitGroups = kGroup == 128 ? 1 : 2;
+  static constexpr int kUnitsPerStep = kGroup == 32 ? 2 : 1;
+  static constexpr int kUnitCols = kUnitGroups * NT;
+  static constexpr int kSlots = 256 / kUnitCols >= 4 ? 4 : 2;  // units' sums in tensor memory
+  static constexpr uint32_t kUnpackedCol = 256;      // kSteps x 64 columns
+  static constexpr int kSumBytes = 2 * NT * kTcRows * 4;
+  static_assert(kSlots * kUnitCols <= 256, "tensor memory");
+  static_assert(kSumBytes <= kStages * int(kCodeBytes), "the sums fit in the codes' ring");
+  // a row's scales: padded so that 16-byte reads of 8 rows touch 32 banks
+  static constexpr int scale_pitch(int K) { return K / 2 / kGroup * 2 + 16; }
+  static constexpr int smem_bytes(int K) {
+    return 1024 + kStages * int(kCodeBytes) + kSteps * 2 * int(kXHalf) + kTcRows * scale_pitch(K);
   }
+};
+
+// 8 codes (low nibble of byte 0 first) to 4 pairs of bf16 integers.
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t* out) {
+  const uint32_t hi = w >> 4;
+  const uint32_t m = 0x43084308u;  // 136
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // byte i's low nibble in the low half, its high nibble in the high half
+    const uint32_t v = (__byte_perm(w, hi, i | i << 4 | (4 + i) << 8 | (4 + i) << 12) & 0x000f000fu) |
+                       0x43004300u;
+    const __nv_bfloat162 r = __hsub2(reinterpret_cast<const __nv_bfloat162&>(v),
+                                     reinterpret_cast<const __nv_bfloat162&>(m));
+    out[i] = reinterpret_cast<const uint32_t&>(r);
+  }
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// acc[0 .. C) += s * the C columns at taddr. done() runs once they have been read.
+template <int C, class Done>
+__device__ __forceinline__ void scale_add(uint32_t taddr, float s, float* acc, Done done) {
+  uint32_t v[C];
+  if constexpr (C == 32) {
+    tmem_ld32(taddr, v);
+  } else {
+    static_assert(C == 16, "columns");
+    tmem_ld16(taddr, v);
+  }
+  tmem_ld_wait();
+  reg_fence(v);
+  done();
+#pragma unroll
+  for (int i = 0; i < C; ++i) acc[i] = fmaf(__uint_as_float(v[i]), s, acc[i]);
+}
+
+// The rare part of a wait stays out of line.
+__device__ __forceinline__ bool w4_wait_more(uint64_t* bar, uint32_t parity, const WaitCtl ctl,
+                                          uint32_t site) {
+  return mbar_wait(bar, parity, ctl, site);
+}
+
+__device__ __forceinline__ bool w4_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl,
+                                        uint32_t site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, w4_wait_more(bar, parity, ctl, site));
+}
+
+// An MMA (A in tensor memory) and a commit, issued by the lane with el != 0 of a
+// warp that runs as a whole: its operands stay in uniform registers.
+__device__ __forceinline__ void mma_ts_el(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bd), "r"(idesc), "r"(accumulate), "r"(el)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_el(uint64_t* bar, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(el)
+      : "memory");
+}
+
+template <int NT, int kGroup>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+    oproj_w4_tc_kernel(const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ CUtensorMap tmQ,
+                       const __nv_bfloat16* __restrict__ scale, __nv_bfloat16* __restrict__ C,
+                       int64_t M, int N, int K, unsigned long long wait_limit_ns,
+                       unsigned int* err_word, int test_stall) {
+  using Cfg = TcCfg<NT, kGroup>;
+  constexpr int kStages = Cfg::kStages, kSteps = Cfg::kSteps, kSlots = Cfg::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t codes_full[kStages], codes_empty[kStages];
+  __shared__ uint64_t step_full[kSteps], step_free[kSteps];  // x and unpacked codes
+  __shared__ uint64_t sums_full[kSlots], sums_empty[kSlots];
+  __shared__ uint64_t drain_bar[kIssuers];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* xring = smem + kStages * Cfg::kCodeBytes;
+  uint8_t* scales = xring + kSteps * 2 * Cfg::kXHalf;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int n0 = int(blockIdx.x >> 1) * kTcRows;
+  const int64_t m0 = int64_t(blockIdx.y) * NT;
+  const int half = K / 2, k0 = int(rank) * half;
+  const int stages = half / 256, steps = half / 128;
+  const int pitch = Cfg::scale_pitch(K);
+  WaitCtl ctl{&abort_flag, wait_limit_ns, kErrKernelOprojW4, err_word};
+
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&codes_full[i], 1);
+      mbar_init(&codes_empty[i], 8);
+    }
+    for (int i = 0; i < kSteps; ++i) {
+      mbar_init(&step_full[i], 5);  // the copy of x and four warps
+      mbar_init(&step_free[i], Cfg::kUnitsPerStep);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sums_full[i], 1);
+      mbar_init(&sums_empty[i], 4);
+    }
+    for (int i = 0; i < kIssuers; ++i) mbar_init(&drain_bar[i], 1);
+    fence_barrier_init();
+  }
+  if (warp == 16) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp < 8) {
+    setmaxnreg_dec<kRegsUnpack>();
+    // ------------------------------------------------- unpack codes: warps 0-3 the
+    // first 128 features of a stage, 4-7 the others; thread = weight row
+    const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+    for (int i = 0; i < stages; ++i) {
+      const int stage = i % kStages, st = 2 * i + wg, buf = st % kSteps;
+      if (!w4_wait(&codes_full[stage], uint32_t(i / kStages) & 1u, ctl, 1)) break;
+      const uint8_t* c = smem + stage * Cfg::kCodeBytes + row * 128;
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = *reinterpret_cast<const uint4*>(c + (((wg * 4 + j) ^ (row & 7)) << 4));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&codes_empty[stage]);
+      if (!w4_wait(&step_free[buf], (uint32_t(st / kSteps) & 1u) ^ 1u, ctl, 2)) break;
+      tc_fence_after();
+      const uint32_t dst = tmem_addr(tmem, quad * 32, Cfg::kUnpackedCol + buf * 64);
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t a[32];
+        const uint32_t ws[8] = {w[j].x,     w[j].y,     w[j].z,     w[j].w,
+                                w[j + 1].x, w[j + 1].y, w[j + 1].z, w[j + 1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) unpack8(ws[e], a + 4 * e);
+        tmem_st32(dst + j * 16, a);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&step_full[buf]);
+    }
+  } else if (warp < 16) {
+    setmaxnreg_inc<kRegsAdd>();
+    // ------------------------------------------------- scale and add; thread = weight row
+    const int wg = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
+    constexpr int kUG = Cfg::kUnitGroups;
+    {
+      // this warp's 16 rows of scales (the other group's warp has the rest)
+      const int pieces = half / kGroup / 8;  // 16-byte pieces of a row
+      const int r0 = quad * 32 + wg * 16;
+      for (int i = lane; i < 16 * pieces; i += 32) {
+        const int r = r0 + i / pieces, c = i % pieces;
+        cp16(smem_u32(scales + r * pitch + c * 16),
+             scale + size_t(n0 + r) * (K / kGroup) + k0 / kGroup + c * 8);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      named_barrier_sync(1, 256);
+    }
+    float acc[NT] = {};
+    bool ok = true;
+    const int blocks = half / kGroup / 8;  // eight groups each
+    int use = 0;                           // units this warp has taken
+    for (int b = 0; b < blocks && ok; ++b) {
+      const uint4 s4 = *reinterpret_cast<const uint4*>(scales + row * pitch + b * 16);
+      const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int h = 0; h < 4 / kUG; ++h, ++use) {
+        // unit 2 use + wg: its groups' place in the eight is (2 h + wg) kUG
+        const int slot = (2 * use + wg) % kSlots;
+        ok = mbar_wait_warp(&sums_full[slot], uint32_t((2 * use + wg) / kSlots) & 1u, ctl, 3);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < kUG; ++g) {
+          uint32_t pair;
+          bool high;
+          if (kUG == 2) {
+            pair = wg ? sw[2 * h + 1] : sw[2 * h];
+            high = g == 1;
+          } else {
+            pair = sw[h];
+            high = wg == 1;
+          }
+          const float s = __uint_as_float(high ? pair & 0xffff0000u : pair << 16);
+          const uint32_t src = tmem_addr(tmem, quad * 32, slot * Cfg::kUnitCols + g * NT);
+          auto nothing = [] {};
+          auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sums_empty[slot]);
+          };
+          constexpr int kLast = NT == 32 ? 32 : 16;
+#pragma unroll
+          for (int c = 0; c + kLast < NT; c += kLast) scale_add<kLast>(src + c, s, acc + c, nothing);
+          if (g == kUG - 1)
+            scale_add<kLast>(src + NT - kLast, s, acc + NT - kLast, release);
+          else
+            scale_add<kLast>(src + NT - kLast, s, acc + NT - kLast, nothing);
+        }
+      }
+    }
+    // Every MMA is done, so the codes' ring is free: [warps' half][token][row].
+    if (named_barrier_and(1, 256, ok)) {  // (once both groups are past their last unit)
+      float* sum = reinterpret_cast<float*>(smem) + wg * NT * kTcRows + row;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) sum[i * kTcRows] = acc[i];
+    }
+  } else {
+    setmaxnreg_dec<kRegsIssue>();
+    if (warp < 16 + kIssuers) {
+    // ------------------------------------------------- issue the MMAs of every other
+    // unit (a unit's waits take as long as its MMAs). Each issuer meets the phases
+    // of the barriers it waits on in order: units of one parity share slots.
+    constexpr uint32_t idesc = idesc_bf16_f32(kTcRows, NT, false, false);
+    constexpr int kUnitK = kGroup * Cfg::kUnitGroups;  // features of a unit
+    const uint32_t el = elect_one() ? 1u : 0u;
+    const uint64_t x_desc = sdesc_sw128(smem_u32(xring), 16, 1024);
+    const int issuer = warp - 16, units = steps * Cfg::kUnitsPerStep;
+    for (int unit = issuer; unit < units; unit += kIssuers) {
+      const int st = unit / Cfg::kUnitsPerStep, buf = st % kSteps, slot = unit % kSlots;
+      const int k0 = Cfg::kUnitsPerStep == 2 ? issuer * (kUnitK / 16) : 0;  // of the step, in 16s
+      if (!w4_wait(&step_full[buf], uint32_t(st / kSteps) & 1u, ctl, 4)) break;
+      if (!w4_wait(&sums_empty[slot], (uint32_t(unit / kSlots) & 1u) ^ 1u, ctl, 6)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + slot * Cfg::kUnitCols;
+      const uint32_t a = tmem + Cfg::kUnpackedCol + buf * 64 + k0 * 8;
+      const uint64_t x = x_desc + ((buf * 2 * Cfg::kXHalf + k0 / 4 * Cfg::kXHalf) >> 4);
+#pragma unroll
+      for (int k = 0; k < kUnitK / 16; ++k)
+        mma_ts_el(d + k / (kGroup / 16) * NT, a + k * 8,
+                  x + ((k / 4 * Cfg::kXHalf + k % 4 * 32) >> 4), idesc, k % (kGroup / 16) != 0, el);
+      commit_el(&sums_full[slot], el);
+      commit_el(&step_free[buf], el);
+    }
+    // Nothing may be in flight when tensor memory is released.
+    commit_el(&drain_bar[issuer], el);
+    int zero = 0;
+    w4_wait(&drain_bar[issuer], 0, WaitCtl{&zero, wait_limit_ns, kErrKernelOprojW4, err_word}, 7);
+    } else if (warp == 16 + kIssuers && lane == 0) {
+    // ------------------------------------------------- loads
+    prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmQ);
+    int codes = 0, xs = 0;  // copies issued
+    auto next_codes = [&] {
+      const int stage = codes % kStages;
+      if (!mbar_wait(&codes_empty[stage], (uint32_t(codes / kStages) & 1u) ^ 1u, ctl, 8)) return false;
+      mbar_arrive_expect_tx(&codes_full[stage], Cfg::kCodeBytes);
+      tma_load_2d(smem + stage * Cfg::kCodeBytes, &tmQ, &codes_full[stage], k0 / 2 + codes * 128, n0);
+      ++codes;
+      return true;
+    };
+    auto next_x = [&] {
+      const int buf = xs % kSteps;
+      if (!mbar_wait(&step_free[buf], (uint32_t(xs / kSteps) & 1u) ^ 1u, ctl, 9)) return false;
+      mbar_arrive_expect_tx(&step_full[buf], 2 * Cfg::kXHalf);
+      uint8_t* dst = xring + buf * 2 * Cfg::kXHalf;
+      tma_load_2d(dst, &tmX, &step_full[buf], k0 + xs * 128, int(m0));
+      tma_load_2d(dst + Cfg::kXHalf, &tmX, &step_full[buf], k0 + xs * 128 + 64, int(m0));
+      ++xs;
+      return true;
+    };
+    // (the failure-detection test's first CTA loads nothing: its waits run out)
+    bool ok = !(test_stall && blockIdx.x == 0 && blockIdx.y == 0);
+    // the codes run ahead of x, which waits for the MMAs
+    for (int i = 0; i < kStages - 1 && i < stages && ok; ++i) ok = next_codes();
+    for (int i = 0; i < stages && ok; ++i) {
+      ok = next_x() && next_x();
+      if (ok && codes < stages) ok = next_codes();
+    }
+    if (!ok) {
+      // every copy has landed before the CTA leaves
+      int zero = 0;
+      WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
+      for (int i = codes > kStages ? codes - kStages : 0; i < codes; ++i)
+        mbar_wait(&codes_full[i % kStages], uint32_t(i / kStages) & 1u, drain, 10);
+      for (int i = xs > kSteps ? xs - kSteps : 0; i < xs; ++i)
+        mbar_wait(&step_full[i % kSteps], uint32_t(i / kSteps) & 1u, drain, 11);
+    }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  // Half of the tokens each: the sums of both CTAs.
+  const uint32_t peer = mapa_shared(smem_u32(smem), rank ^ 1);
+  if (!abort_flag && !ld_shared_cluster_u32(mapa_shared(smem_u32(&abort_flag), rank ^ 1))) {
+    for (int i = tid; i < NT / 2 * (kTcRows / 4); i += kTcThreads) {
+      const int tok = int(rank) * (NT / 2) + i / (kTcRows / 4), r = i % (kTcRows / 4) * 4;
+      if (m0 + tok >= M) break;
+      const uint32_t off = uint32_t(tok * kTcRows + r) * 4;
+      auto own = [&](int g) {
+        return *reinterpret_cast<const float4*>(smem + off + g * (Cfg::kSumBytes / 2));
+      };
+      const float4 p = own(0), q = own(1);
+      const float4 u = ld_shared_cluster_f4(peer + off);
+      const float4 w = ld_shared_cluster_f4(peer + off + Cfg::kSumBytes / 2);
+      uint2 o;
+      o.x = pack_bf16x2((p.x + q.x) + (u.x + w.x), (p.y + q.y) + (u.y + w.y));
+      o.y = pack_bf16x2((p.z + q.z) + (u.z + w.z), (p.w + q.w) + (u.w + w.w));
+      *reinterpret_cast<uint2*>(C + (m0 + tok) * N + n0 + r) = o;
+    }
+  }
+  cluster_sync();  // neither CTA leaves while the other reads its sums
+}
+
+template <int NT, int kGroup>
+cudaError_t launch_tc(const void* A, const void* q, const void* scale, void* C, int64_t M, int N,
+                      int K, unsigned long long wait_limit_ns, unsigned int* err_word,
+                      int test_stall, cudaStream_t stream) {
+  CUtensorMap tmX, tmQ;
+  const uint64_t x_dims[2] = {uint64_t(K), uint64_t(M)}, x_strides[1] = {uint64_t(K) * 2};
+  const uint32_t x_box[2] = {64, NT};  // tokens past M read as zero
+  const uint64_t q_dims[2] = {uint64_t(K / 2), uint64_t(N)}, q_strides[1] = {uint64_t(K / 2)};
+  const uint32_t q_box[2] = {128, kTcRows};
+  if (!encode_tmap_bf16(&tmX, A, 2, x_dims, x_strides, x_box, true) ||
+      !encode_tmap_u8(&tmQ, q, 2, q_dims, q_strides, q_box, true))
+    return cudaErrorInvalidValue;
+  auto kern = oproj_w4_tc_kernel<NT, kGroup>;
+  const int bytes = TcCfg<NT, kGroup>::smem_bytes(K);
+  static ContextCache attr;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), bytes, &attr);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(unsigned(N / kTcRows) * 2, unsigned((M + NT - 1) / NT));
+  kern<<<grid, kTcThreads, bytes, stream>>>(tmX, tmQ, static_cast<const __nv_bfloat16*>(scale),
+                                            static_cast<__nv_bfloat16*>(C), M, N, K, wait_limit_ns,
+                                            err_word, test_stall);
+  return cudaGetLastError();
+}
+
+// Up to 8 tokens the streams of the first kernel (M = 8: 18.9, 17.4 and 17.9 us
+// with groups of 32, 64 and 128; the tensor-core kernel 21.2, 19.7 and 18.8); from
+// 9 on the other (M = 16: 21.2, 19.7 and 19.1 us against 25.0, 23.9 and 22.8), in
+// passes of equal width, 64 tokens at most.
+template <int kGroup>
+cudaError_t launch_group(const void* A, const void* q, const void* scale, void* C, int64_t M, int N,
+                         int K, unsigned long long wait_limit_ns, unsigned int* err_word,
+                         int test_stall, cudaStream_t stream) {
+  if (M <= 8) return launch_stream<kGroup>(A, q, scale, C, M, N, K, stream);
+  auto launch = launch_tc<64, kGroup>;
+  const int64_t passes = (M + 63) / 64;
+  switch ((M + 16 * passes - 1) / (16 * passes)) {
+    case 1: launch = launch_tc<16, kGroup>; break;
+    case 2: launch = launch_tc<32, kGroup>; break;
+    case 3: launch = launch_tc<48, kGroup>; break;
+    default: break;
+  }
+  return launch(A, q, scale, C, M, N, K, wait_limit_ns, err_word, test_stall, stream);
 }
 
 }  // namespace
@@ -338,12 +699,16 @@ cudaError_t launch_quant_weight_w4(const void* W, int N, int K, int group, void*
 }
 
 cudaError_t launch_oproj_w4(const void* A, const void* q, const void* scale, int group, void* C,
-                            int64_t M, int N, int K, cudaStream_t stream) {
-  if (N % 64 != 0 || K % (2 * kW4Warps * kW4Step) != 0 || M < 1) return cudaErrorInvalidValue;
+                            int64_t M, int N, int K, unsigned long long wait_limit_ns,
+                            unsigned int* err_word, int test_stall, cudaStream_t stream) {
+  if (N % 128 != 0 || K % (2 * kW4Warps * kW4Step) != 0 || M < 1) return cudaErrorInvalidValue;
   switch (group) {
-    case 32: return launch_group<32>(A, q, scale, C, M, N, K, stream);
-    case 64: return launch_group<64>(A, q, scale, C, M, N, K, stream);
-    case 128: return launch_group<128>(A, q, scale, C, M, N, K, stream);
+    case 32:
+      return launch_group<32>(A, q, scale, C, M, N, K, wait_limit_ns, err_word, test_stall, stream);
+    case 64:
+      return launch_group<64>(A, q, scale, C, M, N, K, wait_limit_ns, err_word, test_stall, stream);
+    case 128:
+      return launch_group<128>(A, q, scale, C, M, N, K, wait_limit_ns, err_word, test_stall, stream);
     default: return cudaErrorInvalidValue;
   }
 }

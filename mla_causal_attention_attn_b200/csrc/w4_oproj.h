@@ -12,8 +12,10 @@ namespace mla {
 cudaError_t launch_quant_weight_w4(const void* W, int N, int K, int group, void* q, void* scale,
                                    cudaStream_t stream);
 
-// C[M, N] = A[M, K] . W^T with W = (code - 8) * scale. N % 64 == 0, K % 2048 == 0.
+// C[M, N] = A[M, K] . W^T with W = (code - 8) * scale. N % 128 == 0, K % 2048 == 0.
+// Waits that run out are reported in err_word.
 cudaError_t launch_oproj_w4(const void* A, const void* q, const void* scale, int group, void* C,
-                            int64_t M, int N, int K, cudaStream_t stream);
+                            int64_t M, int N, int K, unsigned long long wait_limit_ns,
+                            unsigned int* err_word, int test_stall, cudaStream_t stream);
 
 }  // namespace mla
