@@ -274,17 +274,18 @@ cudaError_t launch_stream(const void* A, const void* q, const void* scale, void*
 // 32 or 64 features, one of 128; even units go to the first four warps, odd ones
 // to the others. The four partial sums meet in shared memory, the cluster's
 // included, in a fixed order.
-constexpr int kTcThreads = 640;  // 8 warps unpack, 8 scale and add, 2 issue MMAs, 1 loads
+constexpr int kTcThreads = 640;  // 8 warps unpack, 8 scale and add, 2 issue MMAs, 2 load
 // 640 threads get 96 registers each; the warpgroups share them out:
 // 2 x 128 x 80 + 2 x 128 x 136 + 128 x 48 = 640 x 96.
 constexpr uint32_t kRegsUnpack = 80, kRegsAdd = 136, kRegsIssue = 48;
-constexpr int kIssuers = 2;
+constexpr int kIssuers = 2, kCodesWarp = 16 + kIssuers;
 constexpr int kTcRows = 128;
 
 template <int NT, int kGroup>
 struct TcCfg {
-  static constexpr int kStages = 5;                  // 256 features of codes
-  static constexpr int kSteps = 4;                   // 128 features of x and unpacked codes
+  static constexpr int kStages = 6;                  // 256 features of codes
+  static constexpr int kSteps = 4;                   // 128 features of unpacked codes
+  static constexpr int kXSteps = NT == 64 ? 4 : NT == 48 ? 6 : 8;  // 128 features of x
   static constexpr uint32_t kCodeBytes = kTcRows * 128;
   static constexpr uint32_t kXHalf = NT * 128;       // 64 features of the tokens
   static constexpr int kUnitGroups = kGroup == 128 ? 1 : 2;
@@ -298,7 +299,7 @@ struct TcCfg {
   // a row's scales: padded so that 16-byte reads of 8 rows touch 32 banks
   static constexpr int scale_pitch(int K) { return K / 2 / kGroup * 2 + 16; }
   static constexpr int smem_bytes(int K) {
-    return 1024 + kStages * int(kCodeBytes) + kSteps * 2 * int(kXHalf) + kTcRows * scale_pitch(K);
+    return 1024 + kStages * int(kCodeBytes) + kXSteps * 2 * int(kXHalf) + kTcRows * scale_pitch(K);
   }
 };
 
@@ -327,21 +328,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-// acc[0 .. C) += s * the C columns at taddr. done() runs once they have been read.
-template <int C, class Done>
-__device__ __forceinline__ void scale_add(uint32_t taddr, float s, float* acc, Done done) {
-  uint32_t v[C];
-  if constexpr (C == 32) {
+template <int C>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[C]) {
+  if constexpr (C == 32)
     tmem_ld32(taddr, v);
-  } else {
-    static_assert(C == 16, "columns");
+  else
     tmem_ld16(taddr, v);
-  }
-  tmem_ld_wait();
-  reg_fence(v);
-  done();
-#pragma unroll
-  for (int i = 0; i < C; ++i) acc[i] = fmaf(__uint_as_float(v[i]), s, acc[i]);
 }
 
 // The rare part of a wait stays out of line.
@@ -388,16 +380,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                        unsigned int* err_word, int test_stall) {
   using Cfg = TcCfg<NT, kGroup>;
   constexpr int kStages = Cfg::kStages, kSteps = Cfg::kSteps, kSlots = Cfg::kSlots;
+  constexpr int kXSteps = Cfg::kXSteps;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t codes_full[kStages], codes_empty[kStages];
-  __shared__ uint64_t step_full[kSteps], step_free[kSteps];  // x and unpacked codes
+  __shared__ uint64_t x_full[kXSteps], x_free[kXSteps];
+  __shared__ uint64_t step_full[kSteps], step_free[kSteps];  // unpacked codes
   __shared__ uint64_t sums_full[kSlots], sums_empty[kSlots];
   __shared__ uint64_t drain_bar[kIssuers];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* xring = smem + kStages * Cfg::kCodeBytes;
-  uint8_t* scales = xring + kSteps * 2 * Cfg::kXHalf;
+  uint8_t* scales = xring + kXSteps * 2 * Cfg::kXHalf;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
@@ -408,14 +402,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const int pitch = Cfg::scale_pitch(K);
   WaitCtl ctl{&abort_flag, wait_limit_ns, kErrKernelOprojW4, err_word};
 
-  if (tid == 0) {
+  int codes = 0, xs = 0;  // copies issued
+  auto next_codes = [&] {
+    const int stage = codes % kStages;
+    if (!mbar_wait(&codes_empty[stage], (uint32_t(codes / kStages) & 1u) ^ 1u, ctl, 8)) return false;
+    mbar_arrive_expect_tx(&codes_full[stage], Cfg::kCodeBytes);
+    tma_load_2d(smem + stage * Cfg::kCodeBytes, &tmQ, &codes_full[stage], k0 / 2 + codes * 128, n0);
+    ++codes;
+    return true;
+  };
+  auto next_x = [&] {
+    const int buf = xs % kXSteps;
+    if (!mbar_wait(&x_free[buf], (uint32_t(xs / kXSteps) & 1u) ^ 1u, ctl, 9)) return false;
+    mbar_arrive_expect_tx(&x_full[buf], 2 * Cfg::kXHalf);
+    uint8_t* dst = xring + buf * 2 * Cfg::kXHalf;
+    tma_load_2d(dst, &tmX, &x_full[buf], k0 + xs * 128, int(m0));
+    tma_load_2d(dst + Cfg::kXHalf, &tmX, &x_full[buf], k0 + xs * 128 + 64, int(m0));
+    ++xs;
+    return true;
+  };
+  // (the failure-detection test's first CTA loads nothing: its waits run out)
+  bool loading = !(test_stall && blockIdx.x == 0 && blockIdx.y == 0);
+  if (warp == kCodesWarp && lane == 0) {
+    prefetch_tensormap(&tmQ);
     abort_flag = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&codes_full[i], 1);
-      mbar_init(&codes_empty[i], 8);
+      mbar_init(&codes_empty[i], 4);
+    }
+    for (int i = 0; i < kXSteps; ++i) {
+      mbar_init(&x_full[i], 1);
+      mbar_init(&x_free[i], Cfg::kUnitsPerStep);
     }
     for (int i = 0; i < kSteps; ++i) {
-      mbar_init(&step_full[i], 5);  // the copy of x and four warps
+      mbar_init(&step_full[i], 4);
       mbar_init(&step_free[i], Cfg::kUnitsPerStep);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -424,6 +444,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < kIssuers; ++i) mbar_init(&drain_bar[i], 1);
     fence_barrier_init();
+    // The first copies start before the other warps are ready.
+    if (loading)
+      for (int i = 0; i < kStages && i < stages; ++i) next_codes();
   }
   if (warp == 16) {
     tmem_alloc(&tmem_slot, 512);
@@ -437,34 +460,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   if (warp < 8) {
     setmaxnreg_dec<kRegsUnpack>();
     // ------------------------------------------------- unpack codes: warps 0-3 the
-    // first 128 features of a stage, 4-7 the others; thread = weight row
+    // even stages, 4-7 the odd ones (rings of even length: each slot has one owner,
+    // who meets its phases in order); thread = weight row
     const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-    for (int i = 0; i < stages; ++i) {
-      const int stage = i % kStages, st = 2 * i + wg, buf = st % kSteps;
+    bool ok = true;
+    for (int i = wg; i < stages && ok; i += 2) {
+      const int stage = i % kStages;
       if (!w4_wait(&codes_full[stage], uint32_t(i / kStages) & 1u, ctl, 1)) break;
       const uint8_t* c = smem + stage * Cfg::kCodeBytes + row * 128;
-      uint4 w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = *reinterpret_cast<const uint4*>(c + (((wg * 4 + j) ^ (row & 7)) << 4));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&codes_empty[stage]);
-      if (!w4_wait(&step_free[buf], (uint32_t(st / kSteps) & 1u) ^ 1u, ctl, 2)) break;
-      tc_fence_after();
-      const uint32_t dst = tmem_addr(tmem, quad * 32, Cfg::kUnpackedCol + buf * 64);
+      for (int h = 0; h < 2; ++h) {
+        const int st = 2 * i + h, buf = st % kSteps;
+        uint4 w[4];
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        uint32_t a[32];
-        const uint32_t ws[8] = {w[j].x,     w[j].y,     w[j].z,     w[j].w,
-                                w[j + 1].x, w[j + 1].y, w[j + 1].z, w[j + 1].w};
+        for (int j = 0; j < 4; ++j)
+          w[j] = *reinterpret_cast<const uint4*>(c + (((h * 4 + j) ^ (row & 7)) << 4));
+        ok = w4_wait(&step_free[buf], (uint32_t(st / kSteps) & 1u) ^ 1u, ctl, 2);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dst = tmem_addr(tmem, quad * 32, Cfg::kUnpackedCol + buf * 64);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) unpack8(ws[e], a + 4 * e);
-        tmem_st32(dst + j * 16, a);
+        for (int j = 0; j < 4; j += 2) {
+          uint32_t a[32];
+          const uint32_t ws[8] = {w[j].x,     w[j].y,     w[j].z,     w[j].w,
+                                  w[j + 1].x, w[j + 1].y, w[j + 1].z, w[j + 1].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) unpack8(ws[e], a + 4 * e);
+          tmem_st32(dst + j * 16, a);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        // (the codes' slot is given back once they have been used: an arrive that
+        // follows their loads alone was seen to overtake them)
+        if (lane == 0) {
+          mbar_arrive(&step_full[buf]);
+          if (h == 1) mbar_arrive(&codes_empty[stage]);
+        }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&step_full[buf]);
     }
   } else if (warp < 16) {
     setmaxnreg_inc<kRegsAdd>();
@@ -498,32 +531,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         ok = mbar_wait_warp(&sums_full[slot], uint32_t((2 * use + wg) / kSlots) & 1u, ctl, 3);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t pair = kUG == 2 ? (wg ? sw[2 * h + 1] : sw[2 * h]) : sw[h];
+        const float lo = __uint_as_float(pair << 16), hi = __uint_as_float(pair & 0xffff0000u);
+        const float sg[2] = {kUG == 2 ? lo : wg ? hi : lo, hi};
+        // the unit's columns, a chunk on its way while one is added
+        const uint32_t src = tmem_addr(tmem, quad * 32, slot * Cfg::kUnitCols);
+        constexpr int kCols = Cfg::kUnitCols, kChunk = NT == 64 || kCols % 32 ? 16 : 32;
+        uint32_t v[2][kChunk];
+        tmem_ld_cols(src, v[0]);
 #pragma unroll
-        for (int g = 0; g < kUG; ++g) {
-          uint32_t pair;
-          bool high;
-          if (kUG == 2) {
-            pair = wg ? sw[2 * h + 1] : sw[2 * h];
-            high = g == 1;
+        for (int c = 0; c < kCols / kChunk; ++c) {
+          tmem_ld_wait();
+          reg_fence(v[c & 1]);
+          if (c + 1 < kCols / kChunk) {
+            tmem_ld_cols(src + (c + 1) * kChunk, v[(c + 1) & 1]);
           } else {
-            pair = sw[h];
-            high = wg == 1;
-          }
-          const float s = __uint_as_float(high ? pair & 0xffff0000u : pair << 16);
-          const uint32_t src = tmem_addr(tmem, quad * 32, slot * Cfg::kUnitCols + g * NT);
-          auto nothing = [] {};
-          auto release = [&] {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sums_empty[slot]);
-          };
-          constexpr int kLast = NT == 32 ? 32 : 16;
+          }
 #pragma unroll
-          for (int c = 0; c + kLast < NT; c += kLast) scale_add<kLast>(src + c, s, acc + c, nothing);
-          if (g == kUG - 1)
-            scale_add<kLast>(src + NT - kLast, s, acc + NT - kLast, release);
-          else
-            scale_add<kLast>(src + NT - kLast, s, acc + NT - kLast, nothing);
+          for (int i = 0; i < kChunk; ++i) {
+            const int col = c * kChunk + i;
+            acc[col % NT] = fmaf(__uint_as_float(v[c & 1][i]), sg[col / NT], acc[col % NT]);
+          }
         }
       }
     }
@@ -546,63 +577,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     const int issuer = warp - 16, units = steps * Cfg::kUnitsPerStep;
     for (int unit = issuer; unit < units; unit += kIssuers) {
       const int st = unit / Cfg::kUnitsPerStep, buf = st % kSteps, slot = unit % kSlots;
+      const int xbuf = st % kXSteps;
       const int k0 = Cfg::kUnitsPerStep == 2 ? issuer * (kUnitK / 16) : 0;  // of the step, in 16s
-      if (!w4_wait(&step_full[buf], uint32_t(st / kSteps) & 1u, ctl, 4)) break;
-      if (!w4_wait(&sums_empty[slot], (uint32_t(unit / kSlots) & 1u) ^ 1u, ctl, 6)) break;
+      const uint32_t x_par = uint32_t(st / kXSteps) & 1u, par = uint32_t(st / kSteps) & 1u;
+      const uint32_t sums_par = (uint32_t(unit / kSlots) & 1u) ^ 1u;
+      // (a look takes about 200 clocks here; the three overlap)
+      const bool x_ok = mbar_try_wait(&x_full[xbuf], x_par);
+      const bool step_ok = mbar_try_wait(&step_full[buf], par);
+      const bool sums_ok = mbar_try_wait(&sums_empty[slot], sums_par);
+      if (!__all_sync(0xffffffffu, x_ok && step_ok && sums_ok) &&
+          !(w4_wait(&x_full[xbuf], x_par, ctl, 4) && w4_wait(&step_full[buf], par, ctl, 5) &&
+            w4_wait(&sums_empty[slot], sums_par, ctl, 6)))
+        break;
       tc_fence_after();
       const uint32_t d = tmem + slot * Cfg::kUnitCols;
       const uint32_t a = tmem + Cfg::kUnpackedCol + buf * 64 + k0 * 8;
-      const uint64_t x = x_desc + ((buf * 2 * Cfg::kXHalf + k0 / 4 * Cfg::kXHalf) >> 4);
+      const uint64_t x = x_desc + ((xbuf * 2 * Cfg::kXHalf + k0 / 4 * Cfg::kXHalf) >> 4);
 #pragma unroll
       for (int k = 0; k < kUnitK / 16; ++k)
         mma_ts_el(d + k / (kGroup / 16) * NT, a + k * 8,
                   x + ((k / 4 * Cfg::kXHalf + k % 4 * 32) >> 4), idesc, k % (kGroup / 16) != 0, el);
       commit_el(&sums_full[slot], el);
       commit_el(&step_free[buf], el);
+      commit_el(&x_free[xbuf], el);
     }
     // Nothing may be in flight when tensor memory is released.
     commit_el(&drain_bar[issuer], el);
     int zero = 0;
     w4_wait(&drain_bar[issuer], 0, WaitCtl{&zero, wait_limit_ns, kErrKernelOprojW4, err_word}, 7);
-    } else if (warp == 16 + kIssuers && lane == 0) {
+    } else if (warp == kCodesWarp && lane == 0) {
     // ------------------------------------------------- loads
-    prefetch_tensormap(&tmX);
-    prefetch_tensormap(&tmQ);
-    int codes = 0, xs = 0;  // copies issued
-    auto next_codes = [&] {
-      const int stage = codes % kStages;
-      if (!mbar_wait(&codes_empty[stage], (uint32_t(codes / kStages) & 1u) ^ 1u, ctl, 8)) return false;
-      mbar_arrive_expect_tx(&codes_full[stage], Cfg::kCodeBytes);
-      tma_load_2d(smem + stage * Cfg::kCodeBytes, &tmQ, &codes_full[stage], k0 / 2 + codes * 128, n0);
-      ++codes;
-      return true;
-    };
-    auto next_x = [&] {
-      const int buf = xs % kSteps;
-      if (!mbar_wait(&step_free[buf], (uint32_t(xs / kSteps) & 1u) ^ 1u, ctl, 9)) return false;
-      mbar_arrive_expect_tx(&step_full[buf], 2 * Cfg::kXHalf);
-      uint8_t* dst = xring + buf * 2 * Cfg::kXHalf;
-      tma_load_2d(dst, &tmX, &step_full[buf], k0 + xs * 128, int(m0));
-      tma_load_2d(dst + Cfg::kXHalf, &tmX, &step_full[buf], k0 + xs * 128 + 64, int(m0));
-      ++xs;
-      return true;
-    };
-    // (the failure-detection test's first CTA loads nothing: its waits run out)
-    bool ok = !(test_stall && blockIdx.x == 0 && blockIdx.y == 0);
-    // the codes run ahead of x, which waits for the MMAs
-    for (int i = 0; i < kStages - 1 && i < stages && ok; ++i) ok = next_codes();
-    for (int i = 0; i < stages && ok; ++i) {
-      ok = next_x() && next_x();
-      if (ok && codes < stages) ok = next_codes();
-    }
-    if (!ok) {
+    while (loading && codes < stages) loading = next_codes();
+    if (!loading) {
       // every copy has landed before the CTA leaves
       int zero = 0;
       WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
       for (int i = codes > kStages ? codes - kStages : 0; i < codes; ++i)
         mbar_wait(&codes_full[i % kStages], uint32_t(i / kStages) & 1u, drain, 10);
-      for (int i = xs > kSteps ? xs - kSteps : 0; i < xs; ++i)
-        mbar_wait(&step_full[i % kSteps], uint32_t(i / kSteps) & 1u, drain, 11);
+    }
+    } else if (lane == 0) {
+    while (loading && xs < steps) loading = next_x();
+    if (!loading) {
+      int zero = 0;
+      WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
+      for (int i = xs > kXSteps ? xs - kXSteps : 0; i < xs; ++i)
+        mbar_wait(&x_full[i % kXSteps], uint32_t(i / kXSteps) & 1u, drain, 11);
     }
     }
   }
@@ -616,20 +635,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   // Half of the tokens each: the sums of both CTAs.
   const uint32_t peer = mapa_shared(smem_u32(smem), rank ^ 1);
   if (!abort_flag && !ld_shared_cluster_u32(mapa_shared(smem_u32(&abort_flag), rank ^ 1))) {
-    for (int i = tid; i < NT / 2 * (kTcRows / 4); i += kTcThreads) {
-      const int tok = int(rank) * (NT / 2) + i / (kTcRows / 4), r = i % (kTcRows / 4) * 4;
-      if (m0 + tok >= M) break;
-      const uint32_t off = uint32_t(tok * kTcRows + r) * 4;
-      auto own = [&](int g) {
-        return *reinterpret_cast<const float4*>(smem + off + g * (Cfg::kSumBytes / 2));
-      };
-      const float4 p = own(0), q = own(1);
-      const float4 u = ld_shared_cluster_f4(peer + off);
-      const float4 w = ld_shared_cluster_f4(peer + off + Cfg::kSumBytes / 2);
-      uint2 o;
-      o.x = pack_bf16x2((p.x + q.x) + (u.x + w.x), (p.y + q.y) + (u.y + w.y));
-      o.y = pack_bf16x2((p.z + q.z) + (u.z + w.z), (p.w + q.w) + (u.w + w.w));
-      *reinterpret_cast<uint2*>(C + (m0 + tok) * N + n0 + r) = o;
+    // 512 threads, NT / 32 times 4 rows of a token each, all loads first
+    constexpr int kTimes = (NT + 31) / 32, kPerRow = kTcRows / 4;
+    float4 v[kTimes][4];
+#pragma unroll
+    for (int k = 0; k < kTimes; ++k) {
+      const int i = tid + k * 512, tok = int(rank) * (NT / 2) + i / kPerRow;
+      if (tid < 512 && i < NT / 2 * kPerRow) {
+        const uint32_t off = uint32_t(tok * kTcRows + i % kPerRow * 4) * 4;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          v[k][g] = *reinterpret_cast<const float4*>(smem + off + g * (Cfg::kSumBytes / 2));
+          v[k][2 + g] = ld_shared_cluster_f4(peer + off + g * (Cfg::kSumBytes / 2));
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kTimes; ++k) {
+      const int i = tid + k * 512, tok = int(rank) * (NT / 2) + i / kPerRow;
+      if (tid < 512 && i < NT / 2 * kPerRow && m0 + tok < M) {
+        const float4 &p = v[k][0], &q = v[k][1], &u = v[k][2], &w = v[k][3];
+        uint2 o;  // (own + other: the same sum in either CTA)
+        o.x = pack_bf16x2((p.x + q.x) + (u.x + w.x), (p.y + q.y) + (u.y + w.y));
+        o.y = pack_bf16x2((p.z + q.z) + (u.z + w.z), (p.w + q.w) + (u.w + w.w));
+        *reinterpret_cast<uint2*>(C + (m0 + tok) * N + n0 + i % kPerRow * 4) = o;
+      }
     }
   }
   cluster_sync();  // neither CTA leaves while the other reads its sums
