@@ -568,9 +568,10 @@ mla_status_t mla_attn_tree(const mla_bf16* q_nope, const mla_bf16* q_pe, const m
 
 /*
  * W_o [7168, 8192] bf16 -> W_q [7168, 4096] codes, W_scale [7168, 8192 / group]
- * bf16: scale = bf16(amax / 7) of the group (1 for a group of zeros), code = 8 +
- * the integer nearest to w / scale (fp32 quotient, ties to even), clamped to
- * -8 .. 7. W must be finite. Done once, like loading a checkpoint.
+ * bf16: scale = bf16(amax / 7) of the group, or 1 where that is 0 (a group of
+ * zeros, or of values below bf16's range), code = 8 + the integer nearest to
+ * w / scale (fp32 quotient, ties to even), clamped to -8 .. 7. W must be finite.
+ * Done once, like loading a checkpoint.
  */
 mla_status_t mla_quantize_weight_w4(const mla_bf16* W, int group, uint8_t* W_q, mla_bf16* W_scale,
                                     mla_stream_t stream);
