@@ -1218,12 +1218,11 @@ constexpr int kVLd = kLat + 8;
 constexpr int kVGroups = 8;  // warps that share 64 dims, 64 latent columns each
 constexpr uint32_t kVRows = 2 * kVTok * kVLd * 2;        // a tile's rows, high and low parts
 constexpr uint32_t kVRaw = 2 * kVTok * kLat * 4;         // the next tile's pieces
-constexpr uint32_t value_red(int e) { return kVGroups * kVTok * (e + 4) * 4; }
-constexpr uint32_t value_smem(int e) {
-  // the next tile's pieces; the weights at first, the rows and sums after that
-  const uint32_t w = e * kVLd * 2, later = 2 * kVRows + value_red(e);
-  return kVRaw + (w > later ? w : later);
-}
+constexpr int kE = 64;       // value dims of a CTA
+constexpr uint32_t kVRed = kVGroups * kVTok * (kE + 4) * 4;
+// the next tile's pieces; the weights at first, the rows and sums after that
+constexpr uint32_t kVSmem =
+    kVRaw + (kE * kVLd * 2 > 2 * kVRows + kVRed ? kE * kVLd * 2 : 2 * kVRows + kVRed);
 
 // x as a bf16 and the bf16 of what it leaves: together 2^-17 of x, so that the
 // latent result loses nothing that the output's own rounding would show.
@@ -1251,10 +1250,11 @@ struct RowPlace {
 };
 
 // The latent result of row n, head h, columns 4 (32 c + lane) .. + 3 for c =
-// 0..3, of the pieces j, j + ways, ... only; raw: its first two pieces in
+// 0..3, of the pieces j, j + ways, ... only; raw, raw1: its first two pieces in
 // shared memory.
 __device__ __forceinline__ void join_row(const Scratch& s, const RowPlace& r, int h, int j, int ways,
-                                         int lane, const float4* raw, float4 (&acc)[4]) {
+                                         int lane, const float4* raw, const float4* raw1,
+                                         float4 (&acc)[4]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int pieces = r.at.x;
@@ -1271,7 +1271,7 @@ __device__ __forceinline__ void join_row(const Scratch& s, const RowPlace& r, in
       f0 *= inv;
       f1 *= inv;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = axpy4(f1, raw[kVTok * kLat / 4 + c * 32 + lane], acc[c]);
+      for (int c = 0; c < 4; ++c) acc[c] = axpy4(f1, raw1[c * 32 + lane], acc[c]);
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] = axpy4(f0, raw[c * 32 + lane], acc[c]);
@@ -1300,7 +1300,6 @@ __device__ __forceinline__ void join_row(const Scratch& s, const RowPlace& r, in
   }
 }
 
-template <int kE>
 __global__ void __launch_bounds__(kE * 4, 1)
     tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s) {
   constexpr int kThreads = kE * 4, kWarps = kE / 8, kSplit = 128 / kE;
@@ -1313,7 +1312,7 @@ __global__ void __launch_bounds__(kE * 4, 1)
   auto* rows = reinterpret_cast<__nv_bfloat16*>(rest);      // [2 buffers][high, low][16][kVLd]
   auto* red = reinterpret_cast<float*>(rest + 2 * kVRows);  // [8][16][kRedLd]
   auto* part = reinterpret_cast<float4*>(rest + 2 * kVRows);  // [warps][128]
-  static_assert(kWarps * kLat * 4 <= int(value_red(kE)), "the shares of a row fit");
+  static_assert(kWarps * kLat * 4 <= int(kVRed), "the shares of a row fit");
   __shared__ int live[2][kVTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x / kSplit, e0 = blockIdx.x % kSplit * kE;
@@ -1358,7 +1357,7 @@ __global__ void __launch_bounds__(kE * 4, 1)
     for (int k = 0; k < kOwn; ++k) {
       const int q = warp + k * kWarps;
       float4 acc[4];
-      join_row(s, own[k], h, 0, 1, lane, raw + q * 128, acc);
+      join_row(s, own[k], h, 0, 1, lane, raw + q * 128, raw + (kVTok + q) * 128, acc);
       __nv_bfloat16* so = rows + (2 * buf * kVTok + q) * kVLd;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -1398,7 +1397,8 @@ __global__ void __launch_bounds__(kE * 4, 1)
       r.ml1 = s.part_ml[piece_row(r.at, 1, h)];
     }
     float4 acc[4];
-    join_row(s, r, h, j, ways, lane, raw + min(q, kVTok - 1) * 128, acc);
+    const float4* mine = raw + min(q, kVTok - 1) * 128;
+    join_row(s, r, h, j, ways, lane, mine, mine + kVTok * 128, acc);
 #pragma unroll
     for (int c = 0; c < 4; ++c) part[warp * 128 + c * 32 + lane] = acc[c];
     if (j == 0 && lane == 0 && q < a.N) live[0][q] = r.at.x != 0;
@@ -1459,6 +1459,183 @@ __global__ void __launch_bounds__(kE * 4, 1)
   }
 }
 
+// The same for more tokens, on the tensor cores: D = V_h . o~^T with the head's
+// 128 value dims as the MMA's rows and 32 tokens, high and low parts, as its 64
+// columns. The weights stay in tensor memory as the A operand; a warp joins two
+// rows of a tile into the B operand in shared memory, the next tile's pieces on
+// their way; the results are read back while the next tile's MMAs run.
+constexpr int kTTok = 32;
+constexpr int kTThreads = 512;
+constexpr uint32_t kTRaw = 2 * kTTok * kLat * 4;       // the next tile's pieces
+constexpr uint32_t kTBlk = 2 * kTTok * 128;            // 64 latent columns of the B operand
+constexpr size_t kTSmem = kTRaw + kLat / 64 * kTBlk + 1024;
+constexpr uint32_t kTColD = kLat / 2;                  // tensor memory: weights, then 2 x D
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
+__global__ void __launch_bounds__(kTThreads, 1)
+    tree_value_wide_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
+                           unsigned long long wait_limit_ns, unsigned int* err_word) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t done;      // a tile's MMAs
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ int live[3][kTTok];  // (of three tiles: one is written before all have read the last but one)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* rows = smem;          // [8 column blocks][high 32, low 32][128 bytes], swizzled
+  auto* raw = reinterpret_cast<float4*>(smem + kLat / 64 * kTBlk);  // [2 pieces][32][128]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int quad = warp & 3, part = warp >> 2, h = blockIdx.x;
+  if (tid == 0) {
+    abort_flag = 0;
+    mbar_init(&done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const Waits waits{&abort_flag, err_word, wait_limit_ns};
+  {
+    // thread = value dim: a quarter of its latent columns
+    const auto* w = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(a.w_kv_b) +
+        (size_t(h) * 256 + kNope + quad * 32 + lane) * kLat + part * 128);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t r[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 v = __ldg(w + c * 8 + i);
+        r[4 * i] = v.x;
+        r[4 * i + 1] = v.y;
+        r[4 * i + 2] = v.z;
+        r[4 * i + 3] = v.w;
+      }
+      tmem_st32(tmem_addr(tmem, quad * 32, part * 64 + c * 32), r);
+    }
+    tmem_st_wait();
+  }
+  const int tiles = (a.N + kTTok - 1) / kTTok, step = gridDim.y;
+  RowPlace own[2];
+  auto stage = [&](int tile) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int q = warp + 16 * k, n = tile * kTTok + q;
+      RowPlace& r = own[k];
+      r.at = tile < tiles && n < a.N ? s.row_info[n] : make_int4(0, 0, 0, 0);
+      if (r.at.x == 1 || r.at.x == 2) {
+        const size_t p0 = piece_row(r.at, 0, h), p1 = piece_row(r.at, 1, h);
+        const float* src = r.at.x == 1 ? s.o + (size_t(n) * kHeads + h) * kLat : s.part_o + p0 * kLat;
+        const uint32_t to = smem_u32(raw + q * 128 + lane);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) cp16(to + c * 512, src + (c * 32 + lane) * 4, true);
+        if (r.at.x == 2) {
+          r.ml0 = s.part_ml[p0];
+          r.ml1 = s.part_ml[p1];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            cp16(to + kTTok * kLat * 4 + c * 512, s.part_o + p1 * kLat + (c * 32 + lane) * 4, true);
+        }
+      }
+    }
+    cp_commit();
+  };
+  // Reads the results of the it-th tile back.
+  auto finish = [&](int it, int tile) {
+    tc_fence_after();
+    uint32_t hi[8], lo[8];
+    const uint32_t d = tmem_addr(tmem, quad * 32, kTColD + (it & 1) * 2 * kTTok + part * 8);
+    tmem_ld8(d, hi);
+    tmem_ld8(d + kTTok, lo);
+    tmem_ld_wait();
+    reg_fence(hi);
+    reg_fence(lo);
+    tc_fence_before();
+    auto* out = static_cast<__nv_bfloat16*>(a.out);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      // even lanes store two dims of token i, odd ones of token i + 1
+      const float x = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+      const float y = __uint_as_float(hi[i + 1]) + __uint_as_float(lo[i + 1]);
+      const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
+      const int q = part * 8 + i + (lane & 1);
+      if (live[it % 3][q])
+        *reinterpret_cast<uint32_t*>(out + size_t(tile * kTTok + q) * (kHeads * kVal) + h * kVal +
+                                     quad * 32 + (lane & ~1)) =
+            lane & 1 ? pack_bf16x2(other, y) : pack_bf16x2(x, other);
+    }
+  };
+  constexpr uint32_t idesc = idesc_bf16_f32(kVal, 2 * kTTok, false, false);
+  wait_for_primary();  // (the weights are there already)
+  stage(blockIdx.y);
+  bool ok = true;
+  int it = 0;
+  for (int tile = blockIdx.y; tile < tiles; tile += step, ++it) {
+    cp_wait<0>();
+    __syncwarp();
+    float4 acc[2][4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4* mine = raw + (warp + 16 * k) * 128;
+      join_row(s, own[k], h, 0, 1, lane, mine, mine + kTTok * 128, acc[k]);
+      if (lane == 0) live[it % 3][warp + 16 * k] = own[k].at.x != 0;
+    }
+    __syncwarp();
+    stage(tile + step);
+    if (it > 0) ok = wait_warp(&done, uint32_t(it - 1) & 1u, waits, 40) && ok;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int q = warp + 16 * k;  // (its low parts: row q + 32, the same place in the swizzle)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint8_t* to = rows + (2 * c + (lane >> 4)) * kTBlk + q * 128 +
+                      ((((lane & 15) >> 1) ^ (q & 7)) << 4) + (lane & 1) * 8;
+        split_store(reinterpret_cast<__nv_bfloat16*>(to),
+                    reinterpret_cast<__nv_bfloat16*>(to + kTTok * 128), acc[k][c]);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && ok) {
+      tc_fence_after();
+      const uint32_t d = tmem + kTColD + (it & 1) * 2 * kTTok;
+      const uint64_t desc = sdesc_sw128(smem_u32(rows), 16, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kLat / 16; ++k)
+          mma_ts(d, tmem + k * 8, desc + ((k / 4 * kTBlk + k % 4 * 32) >> 4), idesc, k != 0);
+        mma_commit(&done);
+      }
+      __syncwarp();
+    }
+    if (it > 0) finish(it - 1, tile - step);
+  }
+  // (no row without a tile: N >= 1 and gridDim.y <= tiles)
+  ok = wait_warp(&done, uint32_t(it - 1) & 1u, waits, 41) && ok;
+  finish(it - 1, int(blockIdx.y) + (it - 1) * step);
+  __syncthreads();
+  if (warp == 0) {
+    if (abort_flag) {  // MMAs that were issued may still run
+      int zero = 0;
+      wait_warp(&done, uint32_t(it - 1) & 1u, Waits{&zero, err_word, wait_limit_ns}, 42);
+    }
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 // A launch that may begin while the kernel before it in the stream ends.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem,
@@ -1476,15 +1653,23 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
-template <int kE>
-cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, int y, cudaStream_t stream) {
-  static ContextCache attr;
-  auto kern = tree_value_kernel<kE>;
-  const cudaError_t e =
-      ensure_smem_attr(reinterpret_cast<const void*>(kern), int(value_smem(kE)), &attr);
+// Up to 32 tokens 128 CTAs a tile of 16 (TODO); beyond, a CTA per head walks
+// every other tile of 32 (TODO).
+cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, unsigned long long wait_limit_ns,
+                         unsigned int* err_word, cudaStream_t stream) {
+  static ContextCache attr[2];
+  if (a.N <= 2 * kVTok) {
+    const cudaError_t e =
+        ensure_smem_attr(reinterpret_cast<const void*>(tree_value_kernel), int(kVSmem), &attr[0]);
+    if (e != cudaSuccess) return e;
+    return launch_after(tree_value_kernel, dim3(kHeads * 128 / kE, (a.N + kVTok - 1) / kVTok),
+                        kE * 4, kVSmem, stream, a, s);
+  }
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(tree_value_wide_kernel),
+                                         int(kTSmem), &attr[1]);
   if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3(kHeads * 128 / kE, unsigned(y)), kE * 4, value_smem(kE), stream, a,
-                      s);
+  return launch_after(tree_value_wide_kernel, dim3(kHeads, 2), kTThreads, kTSmem, stream, a, s,
+                      wait_limit_ns, err_word);
 }
 
 }  // namespace
@@ -1541,9 +1726,7 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   e = launch_after(tree_attn_kernel, dim3(2 * clusters), kAThreads, kASmem, stream, tmQ, tmC, tmO,
                    tmPart, a, s, scale_log2, wait_limit_ns, err_word, test_stall);
   if (e != cudaSuccess) return e;
-  const int tiles = (a.N + kVTok - 1) / kVTok;
-  return a.N <= 2 * kVTok ? launch_value<64>(a, s, tiles, stream)
-                          : launch_value<128>(a, s, tiles < 2 ? tiles : 2, stream);
+  return launch_value(a, s, wait_limit_ns, err_word, stream);
 }
 
 }  // namespace mla
