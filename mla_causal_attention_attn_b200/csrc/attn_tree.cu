@@ -1205,24 +1205,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
 }
 
 // ---------------------------------------------------------------- value
-// out[n, h * 128 + e] = sum_r o~[n, h, r] V_h[e, r]: 16 tokens x kE value dims
-// a step. Grid (64 heads * 128 / kE, y): a CTA walks every y-th token tile with
-// its weights in registers, a warp 64 dims x 64 latent columns of them, so that
-// shared memory carries only the rows (with the weights read from it every tile
-// it took 5 us a tile) and the eight warps' sums. The rows of o~ are joined
-// from their pieces first, by one warp a row or, when there are fewer rows than
-// warps, by several that share the pieces; the next tile's rows (of one or two
-// pieces) are copied to shared memory meanwhile.
-constexpr int kVTok = 16;
-constexpr int kVLd = kLat + 8;
-constexpr int kVGroups = 8;  // warps that share 64 dims, 64 latent columns each
-constexpr uint32_t kVRows = 2 * kVTok * kVLd * 2;        // a tile's rows, high and low parts
-constexpr uint32_t kVRaw = 2 * kVTok * kLat * 4;         // the next tile's pieces
-constexpr int kE = 64;       // value dims of a CTA
-constexpr uint32_t kVRed = kVGroups * kVTok * (kE + 4) * 4;
-// the next tile's pieces; the weights at first, the rows and sums after that
-constexpr uint32_t kVSmem =
-    kVRaw + (kE * kVLd * 2 > 2 * kVRows + kVRed ? kE * kVLd * 2 : 2 * kVRows + kVRed);
+// out[n, h * 128 + e] = sum_r o~[n, h, r] V_h[e, r], in two kernels: one for the
+// few rows of a small step, whose time is the latency of joining their pieces,
+// and one on the tensor cores. Both join the rows of o~ from their pieces first.
 
 // x as a bf16 and the bf16 of what it leaves: together 2^-17 of x, so that the
 // latent result loses nothing that the output's own rounding would show.
@@ -1300,170 +1285,132 @@ __device__ __forceinline__ void join_row(const Scratch& s, const RowPlace& r, in
   }
 }
 
-__global__ void __launch_bounds__(kE * 4, 1)
-    tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s) {
-  constexpr int kThreads = kE * 4, kWarps = kE / 8, kSplit = 128 / kE;
-  constexpr int kOwn = kVTok / kWarps;  // a warp's rows of a tile
-  constexpr int kRedLd = kE + 4;
+// Up to 8 rows: grid (64 heads, 2), a CTA computes 64 value dims with mma.sync,
+// its weights in registers, a warp 64 latent columns of them. Several warps join
+// a row (8 / N of them), each some of its pieces.
+constexpr int kFew = 8;
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewDims = 64;
+constexpr int kVLd = kLat + 8;          // padded rows, in elements
+constexpr int kFewRedLd = kFewDims + 4;
+constexpr uint32_t kFewRaw = 2 * kFew * kLat * 4;                // the rows' pieces
+constexpr uint32_t kFewRows = 2 * 16 * kVLd * 2;                 // high and low parts
+constexpr uint32_t kFewRed = kFewWarps * 16 * kFewRedLd * 4;     // the warps' sums
+// (the weights at first, the rows and sums after that)
+constexpr uint32_t kFewSmem = kFewRaw + kFewRows + kFewRed;
+static_assert(kFewDims * kVLd * 2 <= kFewRows + kFewRed, "the weights fit");
+static_assert(kFewWarps * kLat * 4 <= kFewRed, "the shares of a row fit");
+
+__global__ void __launch_bounds__(kFewThreads)
+    tree_value_few_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s) {
   extern __shared__ __align__(16) uint8_t smem[];
-  auto* raw = reinterpret_cast<float4*>(smem);  // [2 pieces][16][128]
-  uint8_t* rest = smem + kVRaw;
+  auto* raw = reinterpret_cast<float4*>(smem);  // [2 pieces][8][128]
+  uint8_t* rest = smem + kFewRaw;
   auto* sw = reinterpret_cast<__nv_bfloat16*>(rest);
-  auto* rows = reinterpret_cast<__nv_bfloat16*>(rest);      // [2 buffers][high, low][16][kVLd]
-  auto* red = reinterpret_cast<float*>(rest + 2 * kVRows);  // [8][16][kRedLd]
-  auto* part = reinterpret_cast<float4*>(rest + 2 * kVRows);  // [warps][128]
-  static_assert(kWarps * kLat * 4 <= int(kVRed), "the shares of a row fit");
-  __shared__ int live[2][kVTok];
+  auto* rows = reinterpret_cast<__nv_bfloat16*>(rest);        // [high, low][16][kVLd]
+  auto* red = reinterpret_cast<float*>(rest + kFewRows);      // [8][16][kFewRedLd]
+  auto* part = reinterpret_cast<float4*>(rest + kFewRows);    // [warps][128]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x / kSplit, e0 = blockIdx.x % kSplit * kE;
-  const auto* w =
-      static_cast<const __nv_bfloat16*>(a.w_kv_b) + (size_t(h) * 256 + kNope + e0) * kLat;
-  for (int i = tid; i < kE * (kLat / 8); i += kThreads) {
+  const int h = blockIdx.x, e0 = blockIdx.y * kFewDims;
+  const auto* w = static_cast<const __nv_bfloat16*>(a.w_kv_b) + (size_t(h) * 256 + kNope + e0) * kLat;
+  for (int i = tid; i < kFewDims * (kLat / 8); i += kFewThreads) {
     const int e = i / (kLat / 8), c = i % (kLat / 8) * 8;
     cp16(smem_u32(sw + e * kVLd + c), w + size_t(e) * kLat + c, true);
   }
   cp_commit();
-  const int tiles = (a.N + kVTok - 1) / kVTok, step = gridDim.y;
-  // Starts the copies of a tile's rows (a warp copies and joins its own).
-  RowPlace own[kOwn];
-  auto stage = [&](int tile) {
+  wait_for_primary();  // (the weights are on their way already)
+  // this warp's row, and its share of the pieces
+  const int ways = kFewWarps / a.N, q = warp / ways, j = warp % ways;
+  RowPlace r{};
+  if (q < a.N) r.at = s.row_info[q];
+  if (r.at.x == 1 || r.at.x == 2) {
+    const size_t p0 = piece_row(r.at, 0, h), p1 = piece_row(r.at, 1, h);
+    const float* src = r.at.x == 1 ? s.o + (size_t(q) * kHeads + h) * kLat : s.part_o + p0 * kLat;
+    if (j == 0) {
+      const uint32_t to = smem_u32(raw + q * 128 + lane);
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-      const int q = warp + k * kWarps, n = tile * kVTok + q;
-      RowPlace& r = own[k];
-      r.at = tile < tiles && n < a.N ? s.row_info[n] : make_int4(0, 0, 0, 0);
-      if (r.at.x == 1 || r.at.x == 2) {
-        const size_t p0 = piece_row(r.at, 0, h), p1 = piece_row(r.at, 1, h);
-        const float* src = r.at.x == 1 ? s.o + (size_t(n) * kHeads + h) * kLat : s.part_o + p0 * kLat;
-        const uint32_t to = smem_u32(raw + q * 128 + lane);
+      for (int c = 0; c < 4; ++c) cp16(to + c * 512, src + (c * 32 + lane) * 4, true);
+      if (r.at.x == 2) {
+        r.ml0 = s.part_ml[p0];
+        r.ml1 = s.part_ml[p1];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) cp16(to + c * 512, src + (c * 32 + lane) * 4, true);
-        if (r.at.x == 2) {
-          r.ml0 = s.part_ml[p0];
-          r.ml1 = s.part_ml[p1];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            cp16(to + kVTok * kLat * 4 + c * 512, s.part_o + p1 * kLat + (c * 32 + lane) * 4, true);
-        }
+        for (int c = 0; c < 4; ++c)
+          cp16(to + kFew * kLat * 4 + c * 512, s.part_o + p1 * kLat + (c * 32 + lane) * 4, true);
       }
     }
-    cp_commit();
-  };
-  // Joins the staged rows into row buffer buf.
-  auto join = [&](int buf) {
-    cp_wait<0>();
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-      const int q = warp + k * kWarps;
-      float4 acc[4];
-      join_row(s, own[k], h, 0, 1, lane, raw + q * 128, raw + (kVTok + q) * 128, acc);
-      __nv_bfloat16* so = rows + (2 * buf * kVTok + q) * kVLd;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        split_store(so + (c * 32 + lane) * 4, so + kVTok * kVLd + (c * 32 + lane) * 4, acc[c]);
-      if (lane == 0) live[buf][q] = own[k].at.x != 0;
-    }
-    __syncwarp();
-  };
-  wait_for_primary();  // (the weights are on their way already)
-  stage(blockIdx.y);
+  }
+  cp_commit();
   cp_wait<1>();
   __syncthreads();
-  // this warp's weights: 8 n-tiles (dims we ..) x 4 steps (columns wk ..)
-  const int we = warp / kVGroups * 64, wk = warp % kVGroups * 64;
+  // this warp's weights: 8 n-tiles x 4 steps (columns wk ..)
+  const int wk = warp * 64;
   uint32_t fw[8][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint32_t r[4];
+    uint32_t f[4];
     // one ldmatrix: 8 dims x 32 columns, two steps
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      ldsm4(r, smem_u32(sw + (we + 8 * i + (lane & 7)) * kVLd + wk + k * 32 + (lane >> 3) * 8));
+      ldsm4(f, smem_u32(sw + (8 * i + (lane & 7)) * kVLd + wk + k * 32 + (lane >> 3) * 8));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) fw[i][4 * k + q] = r[q];
+      for (int e = 0; e < 4; ++e) fw[i][4 * k + e] = f[e];
     }
+  }
+  cp_wait<0>();
+  __syncwarp();
+  const float4* mine = raw + min(q, kFew - 1) * 128;
+  float4 acc[4];
+  join_row(s, r, h, j, ways, lane, mine, mine + kFew * 128, acc);
+  __syncthreads();  // (the weights have been read)
+#pragma unroll
+  for (int c = 0; c < 4; ++c) part[warp * 128 + c * 32 + lane] = acc[c];
+  __syncthreads();
+  for (int i = tid; i < 16 * 128; i += kFewThreads) {
+    const int n = i >> 7, c = i & 127;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n < a.N)
+      for (int k = 0; k < ways; ++k) x = axpy4(1.f, part[(n * ways + k) * 128 + c], x);
+    split_store(rows + n * kVLd + c * 4, rows + (16 + n) * kVLd + c * 4, x);
   }
   __syncthreads();
-  if (tiles == 1 && a.N * 2 <= kWarps) {
-    // fewer rows than warps: several warps a row, each some of its pieces
-    const int ways = kWarps / a.N, q = warp / ways, j = warp % ways;
-    cp_wait<0>();
-    __syncthreads();
-    RowPlace r;
-    r.at = q < a.N ? s.row_info[q] : make_int4(0, 0, 0, 0);
-    if (r.at.x == 2) {
-      r.ml0 = s.part_ml[piece_row(r.at, 0, h)];
-      r.ml1 = s.part_ml[piece_row(r.at, 1, h)];
-    }
-    float4 acc[4];
-    const float4* mine = raw + min(q, kVTok - 1) * 128;
-    join_row(s, r, h, j, ways, lane, mine, mine + kVTok * 128, acc);
+  float d[8][4] = {};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) part[warp * 128 + c * 32 + lane] = acc[c];
-    if (j == 0 && lane == 0 && q < a.N) live[0][q] = r.at.x != 0;
-    __syncthreads();
-    for (int i = tid; i < kVTok * 128; i += kThreads) {
-      const int qq = i >> 7, c = i & 127;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (qq < a.N)
-        for (int k = 0; k < ways; ++k) x = axpy4(1.f, part[(qq * ways + k) * 128 + c], x);
-      split_store(rows + qq * kVLd + c * 4, rows + (kVTok + qq) * kVLd + c * 4, x);
-      if (c == 0 && qq >= a.N) live[0][qq] = 0;
+  for (int k = 0; k < 4; ++k) {
+    uint32_t fa[4];
+    const int at = (lane & 15) * kVLd + wk + k * 16 + (lane >> 4) * 8;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      ldsm4(fa, smem_u32(rows + p * 16 * kVLd + at));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma_16816(d[i], fa, fw[i][2 * k], fw[i][2 * k + 1]);
     }
-  } else {
-    join(0);
   }
-  stage(blockIdx.y + step);
-  int buf = 0;
-  for (int tile = blockIdx.y; tile < tiles; tile += step, buf ^= 1) {
-    __syncthreads();  // the tile's rows are there, the sums are read
-    float d[8][4] = {};
-    const __nv_bfloat16* so = rows + 2 * buf * kVTok * kVLd;
+  // the eight warps' sums
+  float* own = red + warp * 16 * kFewRedLd + (lane >> 2) * kFewRedLd + 2 * (lane & 3);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t fa[4];
-      const int at = (lane & 15) * kVLd + wk + k * 16 + (lane >> 4) * 8;
-      ldsm4(fa, smem_u32(so + at));
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<float2*>(own + 8 * i) = make_float2(d[i][0], d[i][1]);  // (rows 0 .. 7)
+  __syncthreads();
+  const int n = tid / (kFewDims / 4), e = tid % (kFewDims / 4) * 4;
+  if (n < a.N && s.row_info[n].x != 0) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mma_16816(d[i], fa, fw[i][2 * k], fw[i][2 * k + 1]);
-      ldsm4(fa, smem_u32(so + kVTok * kVLd + at));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mma_16816(d[i], fa, fw[i][2 * k], fw[i][2 * k + 1]);
-    }
-    // sum over the warps that share the dims
-    const int g = lane >> 2, t = lane & 3;
-    float* mine = red + (warp % kVGroups) * kVTok * kRedLd + we + 2 * t;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      *reinterpret_cast<float2*>(mine + g * kRedLd + 8 * i) = make_float2(d[i][0], d[i][1]);
-      *reinterpret_cast<float2*>(mine + (g + 8) * kRedLd + 8 * i) = make_float2(d[i][2], d[i][3]);
-    }
-    if (tile + step < tiles) {
-      join(buf ^ 1);
-      stage(tile + 2 * step);
-    }
-    __syncthreads();
-    {
-      static_assert(kVTok * kE / 4 == kThreads, "four dims of a row per thread");
-      const int q = tid / (kE / 4), e = tid % (kE / 4) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kVGroups; ++k)
-        x = axpy4(1.f, *reinterpret_cast<const float4*>(red + (k * kVTok + q) * kRedLd + e), x);
-      if (live[buf][q])
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
-                                  size_t(tile * kVTok + q) * (kHeads * kVal) + h * kVal + e0 + e) =
-            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-    }
+    for (int k = 0; k < kFewWarps; ++k)
+      x = axpy4(1.f, *reinterpret_cast<const float4*>(red + (k * 16 + n) * kFewRedLd + e), x);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + size_t(n) * (kHeads * kVal) +
+                              h * kVal + e0 + e) =
+        make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   }
 }
 
-// The same for more tokens, on the tensor cores: D = V_h . o~^T with the head's
-// 128 value dims as the MMA's rows and 32 tokens, high and low parts, as its 64
-// columns. The weights stay in tensor memory as the A operand; a warp joins two
-// rows of a tile into the B operand in shared memory, the next tile's pieces on
-// their way; the results are read back while the next tile's MMAs run.
+// More rows: D = V_h . o~^T with the head's 128 value dims as the MMA's rows and
+// 32 tokens, high and low parts, as its 64 columns. Grid (64 heads, 1 or 2): a CTA
+// walks every or every other tile of 32 tokens. The weights stay in tensor memory
+// as the A operand; a warp joins two rows of a tile into the B operand in shared
+// memory, the next tile's pieces on their way; the results are read back while
+// the next tile's MMAs run. (With mma.sync a tile of 16 tokens took 2.9 us, 400
+// tokens 36 us.)
 constexpr int kTTok = 32;
 constexpr int kTThreads = 512;
 constexpr uint32_t kTRaw = 2 * kTTok * kLat * 4;       // the next tile's pieces
@@ -1480,7 +1427,7 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 }
 
 __global__ void __launch_bounds__(kTThreads, 1)
-    tree_value_wide_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
+    tree_value_kernel(const __grid_constant__ AttnTreeArgs a, const __grid_constant__ Scratch s,
                            unsigned long long wait_limit_ns, unsigned int* err_word) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t done;      // a tile's MMAs
@@ -1653,23 +1600,23 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
-// Up to 32 tokens 128 CTAs a tile of 16 (TODO); beyond, a CTA per head walks
-// every other tile of 32 (TODO).
+// One row over 131072 keys, 74 pieces: 54 us with the kernel for few rows, 63 with
+// the other one; 16 rows over 509 keys: 27.3 and 25.9; 8 rows the same.
 cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, unsigned long long wait_limit_ns,
                          unsigned int* err_word, cudaStream_t stream) {
   static ContextCache attr[2];
-  if (a.N <= 2 * kVTok) {
-    const cudaError_t e =
-        ensure_smem_attr(reinterpret_cast<const void*>(tree_value_kernel), int(kVSmem), &attr[0]);
+  if (a.N <= kFew) {
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(tree_value_few_kernel),
+                                           int(kFewSmem), &attr[0]);
     if (e != cudaSuccess) return e;
-    return launch_after(tree_value_kernel, dim3(kHeads * 128 / kE, (a.N + kVTok - 1) / kVTok),
-                        kE * 4, kVSmem, stream, a, s);
+    return launch_after(tree_value_few_kernel, dim3(kHeads, kVal / kFewDims), kFewThreads, kFewSmem,
+                        stream, a, s);
   }
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(tree_value_wide_kernel),
-                                         int(kTSmem), &attr[1]);
+  const cudaError_t e =
+      ensure_smem_attr(reinterpret_cast<const void*>(tree_value_kernel), int(kTSmem), &attr[1]);
   if (e != cudaSuccess) return e;
-  return launch_after(tree_value_wide_kernel, dim3(kHeads, 2), kTThreads, kTSmem, stream, a, s,
-                      wait_limit_ns, err_word);
+  return launch_after(tree_value_kernel, dim3(kHeads, a.N > kTTok ? 2 : 1), kTThreads, kTSmem,
+                      stream, a, s, wait_limit_ns, err_word);
 }
 
 }  // namespace
