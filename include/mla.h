@@ -36,8 +36,10 @@
  *        this call's outcome alone; read it with mla_last_device_status();
  *      - calls without a workspace (mla_o_proj, mla_attn_prefill with
  *        workspace NULL, mla_attn_prefill_varlen, mla_kv_up_proj, the FP8
- *        quantisers and GEMM, mla_attn_oproj_noalloc) use one device-wide
- *        word per device, read and cleared atomically by mla_device_status().
+ *        quantisers and GEMM, mla_o_proj_w4, mla_attn_oproj_noalloc) use one
+ *        device-wide word per device, read and cleared atomically by
+ *        mla_device_status(). mla_page_plan, mla_cache_append and
+ *        mla_quantize_weight_w4 wait for nothing and report nothing.
  *  - Device: compute capability 10.0 (B200, sm_100a) only; otherwise
  *    MLA_ERR_UNSUPPORTED_DEVICE.
  *  - Threads: calls are thread-safe. Mutable state shared between calls: the
@@ -515,9 +517,10 @@ mla_status_t mla_cache_append(const mla_bf16* c_kv, const mla_bf16* k_pe,
                               int page_size, int64_t page_stride, mla_stream_t stream);
 
 /*
- * Workspace bytes of mla_attn_tree: the status word, the schedule (48 bytes a
- * request), queries and outputs in latent form (N * 64 * (576 + 512) * 2) and
- * 38 MiB of partial results. Returns 0 for B or N out of range.
+ * Workspace bytes of mla_attn_tree: the status word, the schedule (6.5 KB, 32
+ * bytes a request and 20 a row), the queries (bf16) and results (fp32) in latent
+ * form (N * 64 * (576 * 2 + 512 * 4)) and 37.1 MiB of partial results. Returns 0
+ * for B or N out of range.
  */
 size_t mla_attn_tree_workspace_bytes(int B, int64_t N);
 
@@ -579,8 +582,8 @@ mla_status_t mla_quantize_weight_w4(const mla_bf16* W, int group, uint8_t* W_q, 
 /*
  *   attn [M, 8192] bf16, W_q and W_scale as above, group 32, 64 or 128 (else
  *   MLA_ERR_SHAPE), out [M, 7168] bf16, M 1 .. 2^20. All pointers 16-byte
- *   aligned. Meant for M up to about 128; mla_o_proj is the faster product for
- *   many rows.
+ *   aligned. Meant for M up to about 128 (one reading of W_q per 64 rows);
+ *   mla_o_proj is the faster product for many rows.
  */
 mla_status_t mla_o_proj_w4(const mla_bf16* attn, const uint8_t* W_q, const mla_bf16* W_scale,
                            int group, int64_t M, mla_bf16* out, mla_stream_t stream);
@@ -589,9 +592,9 @@ mla_status_t mla_o_proj_w4(const mla_bf16* attn, const uint8_t* W_q, const mla_b
  * Outcome of the last call that used `workspace` (a workspace given to
  * mla_attn_prefill, mla_attn_oproj, mla_attn_oproj_varlen,
  * mla_attn_prefill_rope, mla_attn_oproj_rope, mla_attn_oproj_latent,
- * mla_attn_oproj_fp8 or mla_attn_tree; that call
- * must have been enqueued on `stream` or be complete). Synchronises `stream`, then reads the call's status word.
- * Returns MLA_ERR_TIMEOUT if one of that call's kernels gave up on a bounded
+ * mla_attn_oproj_fp8 or mla_attn_tree; that call must have been enqueued on
+ * `stream` or be complete). Synchronises `stream`, then reads the call's status
+ * word. Returns MLA_ERR_TIMEOUT if one of that call's kernels gave up on a bounded
  * wait, MLA_ERR_CUDA if the stream reports an error, MLA_ERR_INVALID_ARG for
  * a NULL workspace, MLA_ERR_MISALIGNED for one not 16-byte aligned, else
  * MLA_OK. The word is not cleared (the next call using the workspace clears
