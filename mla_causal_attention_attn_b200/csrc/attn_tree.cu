@@ -1374,6 +1374,8 @@ __global__ void __launch_bounds__(kFewThreads)
       for (int k = 0; k < ways; ++k) x = axpy4(1.f, part[(n * ways + k) * 128 + c], x);
     split_store(rows + n * kVLd + c * 4, rows + (16 + n) * kVLd + c * 4, x);
   }
+  const int n = tid / (kFewDims / 4), e = tid % (kFewDims / 4) * 4;
+  const bool live = n < a.N && s.row_info[n].x != 0;
   __syncthreads();
   float d[8][4] = {};
 #pragma unroll
@@ -1393,8 +1395,7 @@ __global__ void __launch_bounds__(kFewThreads)
   for (int i = 0; i < 8; ++i)
     *reinterpret_cast<float2*>(own + 8 * i) = make_float2(d[i][0], d[i][1]);  // (rows 0 .. 7)
   __syncthreads();
-  const int n = tid / (kFewDims / 4), e = tid % (kFewDims / 4) * 4;
-  if (n < a.N && s.row_info[n].x != 0) {
+  if (live) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kFewWarps; ++k)

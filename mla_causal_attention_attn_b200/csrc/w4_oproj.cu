@@ -132,7 +132,9 @@ constexpr int kW4Threads = 256;
 constexpr int kW4Warps = 8;
 constexpr int kW4Rows = 16;
 constexpr int kW4Tokens = 8;
+constexpr int kW4K = 8192;         // (constant, so that every address is a base and an offset)
 constexpr int kW4Step = 128;      // features of a step
+constexpr int kW4Steps = kW4K / kW4Warps / kW4Step;
 constexpr int kW4Ring = 4;        // steps on their way
 constexpr int kW4Pitch = kW4Step / 2 * kW4Ring + 16;  // bytes of a row in the ring: 8 rows x 4 words
                                                       // hit 32 banks
@@ -144,30 +146,30 @@ constexpr int kW4Pitch = kW4Step / 2 * kW4Ring + 16;  // bytes of a row in the r
 // the word of 8 features 32 w + 8 t .. + 7 of rows g and g + 8 and of token g;
 // the word gives the pairs (j, j + 4), j = 0..3, for both operands, and 32
 // features never cross a group. Sums of a group are scaled in fp32, the warps'
-// sums meet in shared memory in a fixed order. One token: 15.5 us with groups of
-// 128, 17.2 of 32. (448 CTAs, three to an SM. 64 rows a CTA and clusters of eight
-// over the features took 65 us for 37 tokens, the ring without clusters 37.)
+// sums meet in shared memory in a fixed order. One token: 14.3 us with groups of
+// 128, 14.7 of 32 (15.5 and 17.2 with the feature count a variable: 31 integer
+// instructions for every 32 features of 16 rows, where unpacking takes 18).
 template <int kGroup>
 __global__ void __launch_bounds__(kW4Threads)
     oproj_w4_kernel(const __nv_bfloat16* __restrict__ A, const uint8_t* __restrict__ q,
                     const __nv_bfloat16* __restrict__ scale, __nv_bfloat16* __restrict__ C, int M,
-                    int N, int K) {
+                    int N) {
+  constexpr int K = kW4K, steps = kW4Steps;
   __shared__ __align__(16) uint8_t smem[kW4Warps * kW4Rows * kW4Pitch];
   constexpr int kPer = kW4Step / kGroup;  // groups of a step
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int n0 = int(blockIdx.x) * kW4Rows;
-  const int slice = K / kW4Warps, k0 = warp * slice, steps = slice / kW4Step;
+  const int k0 = warp * (K / kW4Warps);
   uint8_t* ring = smem + warp * kW4Rows * kW4Pitch;
-  const uint8_t* q0 = q + size_t(n0) * (K / 2) + k0 / 2;
+  // this lane's 16-byte piece of rows lane / 4 and lane / 4 + 8
+  const uint8_t* q0 = q + size_t(n0 + g) * (K / 2) + k0 / 2 + t * 16;
+  const uint32_t r0 = smem_u32(ring + g * kW4Pitch + t * 16);
   auto fetch = [&](int step) {  // one group of copies, empty past the last step
     if (step < steps)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = i * 32 + lane, row = c >> 2, piece = c & 3;
-        cp16(smem_u32(ring + row * kW4Pitch + (step % kW4Ring) * 64 + piece * 16),
-             q0 + size_t(row) * (K / 2) + step * 64 + piece * 16);
-      }
+      for (int i = 0; i < 2; ++i)
+        cp16(r0 + i * 8 * kW4Pitch + (step % kW4Ring) * 64, q0 + i * 8 * (K / 2) + step * 64);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kW4Threads)
     if (step >= steps) return;
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-      xs[b][w] = __ldg(reinterpret_cast<const uint4*>(xp + step * kW4Step + w * 32));
+      xs[b][w] = ld_nc_v4_ordered(xp + step * kW4Step + w * 32);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const __nv_bfloat16* p = sp + size_t(h * 8) * (K / kGroup) + step * kPer;
@@ -235,11 +237,8 @@ __global__ void __launch_bounds__(kW4Threads)
     __syncwarp();
     fetch(step + kW4Ring);
   };
-#pragma unroll 1
-  for (int step = 0; step < steps; step += 2) {  // (K % 2048 == 0)
-    one_step(step, 0);
-    one_step(step + 1, 1);
-  }
+#pragma unroll
+  for (int step = 0; step < steps; ++step) one_step(step, step & 1);
   // the warps' sums, [warp][token][row], in the ring's memory
   constexpr int kLd = kW4Rows + 1;
   static_assert(kW4Warps * kW4Tokens * kLd * 4 <= sizeof(smem), "the sums fit");
@@ -260,10 +259,10 @@ __global__ void __launch_bounds__(kW4Threads)
 
 template <int kGroup>
 cudaError_t launch_stream(const void* A, const void* q, const void* scale, void* C, int64_t M,
-                          int N, int K, cudaStream_t stream) {
+                          int N, cudaStream_t stream) {
   oproj_w4_kernel<kGroup><<<N / kW4Rows, kW4Threads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(A), static_cast<const uint8_t*>(q),
-      static_cast<const __nv_bfloat16*>(scale), static_cast<__nv_bfloat16*>(C), int(M), N, K);
+      static_cast<const __nv_bfloat16*>(scale), static_cast<__nv_bfloat16*>(C), int(M), N);
   return cudaGetLastError();
 }
 
@@ -342,18 +341,6 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[C]) {
     tmem_ld32(taddr, v);
   else
     tmem_ld16(taddr, v);
-}
-
-// The rare part of a wait stays out of line.
-__device__ __forceinline__ bool w4_wait_more(uint64_t* bar, uint32_t parity, const WaitCtl ctl,
-                                          uint32_t site) {
-  return mbar_wait(bar, parity, ctl, site);
-}
-
-__device__ __forceinline__ bool w4_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl,
-                                        uint32_t site) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, w4_wait_more(bar, parity, ctl, site));
 }
 
 // An MMA (A in tensor memory) and a commit, issued by the lane with el != 0 of a
@@ -474,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     for (int i = wg; i < stages && ok; i += 2) {
       const int stage = i % kStages;
-      if (!w4_wait(&codes_full[stage], uint32_t(i / kStages) & 1u, ctl, 1)) break;
+      if (!mbar_wait_warp(&codes_full[stage], uint32_t(i / kStages) & 1u, ctl, 1)) break;
       const uint8_t* c = smem + stage * Cfg::kCodeBytes + row * 128;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -483,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           w[j] = *reinterpret_cast<const uint4*>(c + (((h * 4 + j) ^ (row & 7)) << 4));
-        ok = w4_wait(&step_free[buf], (uint32_t(st / kSteps) & 1u) ^ 1u, ctl, 2);
+        ok = mbar_wait_warp(&step_free[buf], (uint32_t(st / kSteps) & 1u) ^ 1u, ctl, 2);
         if (!ok) break;
         tc_fence_after();
         const uint32_t dst = tmem_addr(tmem, quad * 32, Cfg::kUnpackedCol + buf * 64);
@@ -575,62 +562,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   } else {
     setmaxnreg_dec<kRegsIssue>();
     if (warp < 16 + kIssuers) {
-    // ------------------------------------------------- issue the MMAs of every other
-    // unit (a unit's waits take as long as its MMAs). Each issuer meets the phases
-    // of the barriers it waits on in order: units of one parity share slots.
-    constexpr uint32_t idesc = idesc_bf16_f32(kTcRows, NT, false, false);
-    constexpr int kUnitK = kGroup * Cfg::kUnitGroups;  // features of a unit
-    const uint32_t el = elect_one() ? 1u : 0u;
-    const uint64_t x_desc = sdesc_sw128(smem_u32(xring), 16, 1024);
-    const int issuer = warp - 16, units = steps * Cfg::kUnitsPerStep;
-    for (int unit = issuer; unit < units; unit += kIssuers) {
-      const int st = unit / Cfg::kUnitsPerStep, buf = st % kSteps, slot = unit % kSlots;
-      const int xbuf = st % kXSteps;
-      const int k0 = Cfg::kUnitsPerStep == 2 ? issuer * (kUnitK / 16) : 0;  // of the step, in 16s
-      const uint32_t x_par = uint32_t(st / kXSteps) & 1u, par = uint32_t(st / kSteps) & 1u;
-      const uint32_t sums_par = (uint32_t(unit / kSlots) & 1u) ^ 1u;
-      // (a look takes about 200 clocks here; the three overlap)
-      const bool x_ok = mbar_try_wait(&x_full[xbuf], x_par);
-      const bool step_ok = mbar_try_wait(&step_full[buf], par);
-      const bool sums_ok = mbar_try_wait(&sums_empty[slot], sums_par);
-      if (!__all_sync(0xffffffffu, x_ok && step_ok && sums_ok) &&
-          !(w4_wait(&x_full[xbuf], x_par, ctl, 4) && w4_wait(&step_full[buf], par, ctl, 5) &&
-            w4_wait(&sums_empty[slot], sums_par, ctl, 6)))
-        break;
-      tc_fence_after();
-      const uint32_t d = tmem + slot * Cfg::kUnitCols;
-      const uint32_t a = tmem + Cfg::kUnpackedCol + buf * 64 + k0 * 8;
-      const uint64_t x = x_desc + ((xbuf * 2 * Cfg::kXHalf + k0 / 4 * Cfg::kXHalf) >> 4);
+      // ------------------------------------------------- issue the MMAs of every other
+      // unit (a unit's waits take as long as its MMAs). Each issuer meets the phases
+      // of the barriers it waits on in order: units of one parity share slots.
+      constexpr uint32_t idesc = idesc_bf16_f32(kTcRows, NT, false, false);
+      constexpr int kUnitK = kGroup * Cfg::kUnitGroups;  // features of a unit
+      const uint32_t el = elect_one() ? 1u : 0u;
+      const uint64_t x_desc = sdesc_sw128(smem_u32(xring), 16, 1024);
+      const int issuer = warp - 16, units = steps * Cfg::kUnitsPerStep;
+      for (int unit = issuer; unit < units; unit += kIssuers) {
+        const int st = unit / Cfg::kUnitsPerStep, buf = st % kSteps, slot = unit % kSlots;
+        const int xbuf = st % kXSteps;
+        const int k0 = Cfg::kUnitsPerStep == 2 ? issuer * (kUnitK / 16) : 0;  // of the step, in 16s
+        const uint32_t x_par = uint32_t(st / kXSteps) & 1u, par = uint32_t(st / kSteps) & 1u;
+        const uint32_t sums_par = (uint32_t(unit / kSlots) & 1u) ^ 1u;
+        // (a look takes about 200 clocks here; the three overlap)
+        const bool x_ok = mbar_try_wait(&x_full[xbuf], x_par);
+        const bool step_ok = mbar_try_wait(&step_full[buf], par);
+        const bool sums_ok = mbar_try_wait(&sums_empty[slot], sums_par);
+        if (!__all_sync(0xffffffffu, x_ok && step_ok && sums_ok) &&
+            !(mbar_wait_warp(&x_full[xbuf], x_par, ctl, 4) && mbar_wait_warp(&step_full[buf], par, ctl, 5) &&
+              mbar_wait_warp(&sums_empty[slot], sums_par, ctl, 6)))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem + slot * Cfg::kUnitCols;
+        const uint32_t a = tmem + Cfg::kUnpackedCol + buf * 64 + k0 * 8;
+        const uint64_t x = x_desc + ((xbuf * 2 * Cfg::kXHalf + k0 / 4 * Cfg::kXHalf) >> 4);
 #pragma unroll
-      for (int k = 0; k < kUnitK / 16; ++k)
-        mma_ts_el(d + k / (kGroup / 16) * NT, a + k * 8,
-                  x + ((k / 4 * Cfg::kXHalf + k % 4 * 32) >> 4), idesc, k % (kGroup / 16) != 0, el);
-      commit_el(&sums_full[slot], el);
-      commit_el(&step_free[buf], el);
-      commit_el(&x_free[xbuf], el);
-    }
-    // Nothing may be in flight when tensor memory is released.
-    commit_el(&drain_bar[issuer], el);
-    int zero = 0;
-    w4_wait(&drain_bar[issuer], 0, WaitCtl{&zero, wait_limit_ns, kErrKernelOprojW4, err_word}, 7);
+        for (int k = 0; k < kUnitK / 16; ++k)
+          mma_ts_el(d + k / (kGroup / 16) * NT, a + k * 8,
+                    x + ((k / 4 * Cfg::kXHalf + k % 4 * 32) >> 4), idesc, k % (kGroup / 16) != 0, el);
+        commit_el(&sums_full[slot], el);
+        commit_el(&step_free[buf], el);
+        commit_el(&x_free[xbuf], el);
+      }
+      // Nothing may be in flight when tensor memory is released.
+      commit_el(&drain_bar[issuer], el);
+      int zero = 0;
+      mbar_wait_warp(&drain_bar[issuer], 0, WaitCtl{&zero, wait_limit_ns, kErrKernelOprojW4, err_word}, 7);
     } else if (warp == kCodesWarp && lane == 0) {
-    // ------------------------------------------------- loads
-    while (loading && codes < stages) loading = next_codes();
-    if (!loading) {
-      // every copy has landed before the CTA leaves
-      int zero = 0;
-      WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
-      for (int i = codes > kStages ? codes - kStages : 0; i < codes; ++i)
-        mbar_wait(&codes_full[i % kStages], uint32_t(i / kStages) & 1u, drain, 10);
-    }
+      // ------------------------------------------------- loads
+      while (loading && codes < stages) loading = next_codes();
+      if (!loading) {
+        // every copy has landed before the CTA leaves
+        int zero = 0;
+        WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
+        for (int i = codes > kStages ? codes - kStages : 0; i < codes; ++i)
+          mbar_wait(&codes_full[i % kStages], uint32_t(i / kStages) & 1u, drain, 10);
+      }
     } else if (lane == 0) {
-    while (loading && xs < steps) loading = next_x();
-    if (!loading) {
-      int zero = 0;
-      WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
-      for (int i = xs > kXSteps ? xs - kXSteps : 0; i < xs; ++i)
-        mbar_wait(&x_full[i % kXSteps], uint32_t(i / kXSteps) & 1u, drain, 11);
-    }
+      while (loading && xs < steps) loading = next_x();
+      if (!loading) {
+        int zero = 0;
+        WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
+        for (int i = xs > kXSteps ? xs - kXSteps : 0; i < xs; ++i)
+          mbar_wait(&x_full[i % kXSteps], uint32_t(i / kXSteps) & 1u, drain, 11);
+      }
     }
   }
   __syncwarp();
@@ -697,15 +684,15 @@ cudaError_t launch_tc(const void* A, const void* q, const void* scale, void* C, 
   return cudaGetLastError();
 }
 
-// Up to 8 tokens the streams of the first kernel (M = 8: 18.9, 17.4 and 17.9 us
-// with groups of 32, 64 and 128; the tensor-core kernel 21.2, 19.7 and 18.8); from
-// 9 on the other (M = 16: 21.2, 19.7 and 19.1 us against 25.0, 23.9 and 22.8), in
-// passes of equal width, 64 tokens at most.
+// Up to 8 tokens the streams of the first kernel (M = 8: 16.4, 17.1 and 16.0 us
+// with groups of 32, 64 and 128; the tensor-core kernel 20.8, 19.5 and 19.1); from
+// 9 on the other (M = 16: 21.2, 19.7 and 19.1 us against 25.0, 23.9 and 22.8 for
+// streams of 16 tokens), in passes of equal width, 64 tokens at most.
 template <int kGroup>
 cudaError_t launch_group(const void* A, const void* q, const void* scale, void* C, int64_t M, int N,
                          int K, unsigned long long wait_limit_ns, unsigned int* err_word,
                          int test_stall, cudaStream_t stream) {
-  if (M <= 8) return launch_stream<kGroup>(A, q, scale, C, M, N, K, stream);
+  if (M <= 8) return launch_stream<kGroup>(A, q, scale, C, M, N, stream);
   auto launch = launch_tc<64, kGroup>;
   const int64_t passes = (M + 63) / 64;
   switch ((M + 16 * passes - 1) / (16 * passes)) {
@@ -739,7 +726,7 @@ cudaError_t launch_quant_weight_w4(const void* W, int N, int K, int group, void*
 cudaError_t launch_oproj_w4(const void* A, const void* q, const void* scale, int group, void* C,
                             int64_t M, int N, int K, unsigned long long wait_limit_ns,
                             unsigned int* err_word, int test_stall, cudaStream_t stream) {
-  if (N % 128 != 0 || K % (2 * kW4Warps * kW4Step) != 0 || M < 1) return cudaErrorInvalidValue;
+  if (N % 128 != 0 || K != kW4K || M < 1) return cudaErrorInvalidValue;
   switch (group) {
     case 32:
       return launch_group<32>(A, q, scale, C, M, N, K, wait_limit_ns, err_word, test_stall, stream);

@@ -12,7 +12,7 @@ namespace mla {
 cudaError_t launch_quant_weight_w4(const void* W, int N, int K, int group, void* q, void* scale,
                                    cudaStream_t stream);
 
-// C[M, N] = A[M, K] . W^T with W = (code - 8) * scale. N % 128 == 0, K % 2048 == 0.
+// C[M, N] = A[M, K] . W^T with W = (code - 8) * scale. N % 128 == 0, K == 8192.
 // Waits that run out are reported in err_word.
 cudaError_t launch_oproj_w4(const void* A, const void* q, const void* scale, int group, void* C,
                             int64_t M, int N, int K, unsigned long long wait_limit_ns,
