@@ -277,9 +277,10 @@ cudaError_t launch_stream(const void* A, const void* q, const void* scale, void*
 // before the final bf16. A unit is what those warps take at once: two groups of
 // 32 or 64 features, one of 128; even units go to the first four warps, odd ones
 // to the others. The four partial sums meet in shared memory, the cluster's
-// included, in a fixed order. 37 tokens: 24.4 us with groups of 32, 20.1 of 128
-// (without the unpacking, 23.3 and 15.9; without the adding, 22.9 and 19.5; with
-// one MMA a unit, 23.0 and 19.3: all three stages are close to one another).
+// included, in a fixed order. 37 tokens: 24.2 us with groups of 32, 20.0 of 128
+// (before the last step 24.4 and 20.1; without the unpacking 23.3 and 15.9,
+// without the adding 22.9 and 19.5, with one MMA a unit 23.0 and 19.3: all three
+// stages are close to one another).
 // Unpacking without the permutes, as pairs (j, j + 4), would want x permuted too.
 constexpr int kTcThreads = 640;  // 8 warps unpack, 8 scale and add, 2 issue MMAs, 2 load
 // 640 threads get 96 registers each; the warpgroups share them out:
@@ -301,6 +302,7 @@ struct TcCfg {
   static constexpr int kSlots = 256 / kUnitCols >= 4 ? 4 : 2;  // units' sums in tensor memory
   static constexpr uint32_t kUnpackedCol = 256;      // kSteps x 64 columns
   static constexpr int kSumBytes = 2 * NT * kTcRows * 4;
+  static_assert(kSteps == 4 && kStages % 2 == 0, "each unpacking group owns its slots");
   static_assert(kSlots * kUnitCols <= 256, "tensor memory");
   static_assert(kSumBytes <= kStages * int(kCodeBytes), "the sums fit in the codes' ring");
   // a row's scales: padded so that 16-byte reads of 8 rows touch 32 banks
@@ -371,8 +373,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     oproj_w4_tc_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmQ,
                        const __nv_bfloat16* __restrict__ scale, __nv_bfloat16* __restrict__ C,
-                       int64_t M, int N, int K, unsigned long long wait_limit_ns,
-                       unsigned int* err_word, int test_stall) {
+                       int64_t M, int N, unsigned long long wait_limit_ns, unsigned int* err_word,
+                       int test_stall) {
+  constexpr int K = kW4K;
   using Cfg = TcCfg<NT, kGroup>;
   constexpr int kStages = Cfg::kStages, kSteps = Cfg::kSteps, kSlots = Cfg::kSlots;
   constexpr int kXSteps = Cfg::kXSteps;
@@ -392,9 +395,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int n0 = int(blockIdx.x >> 1) * kTcRows;
   const int64_t m0 = int64_t(blockIdx.y) * NT;
-  const int half = K / 2, k0 = int(rank) * half;
-  const int stages = half / 256, steps = half / 128;
-  const int pitch = Cfg::scale_pitch(K);
+  constexpr int half = K / 2, stages = half / 256, steps = half / 128;
+  constexpr int pitch = Cfg::scale_pitch(K);
+  const int k0 = int(rank) * half;
   WaitCtl ctl{&abort_flag, wait_limit_ns, kErrKernelOprojW4, err_word};
 
   int codes = 0, xs = 0;  // copies issued
@@ -459,18 +462,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     // who meets its phases in order); thread = weight row
     const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     bool ok = true;
-    for (int i = wg; i < stages && ok; i += 2) {
-      const int stage = i % kStages;
-      if (!mbar_wait_warp(&codes_full[stage], uint32_t(i / kStages) & 1u, ctl, 1)) break;
+#pragma unroll  // (integer instructions bound this: slots and parities are constants)
+    for (int i = 0; i < stages / 2; ++i) {
+      if (!ok) break;
+      const int stage = 2 * (i % (kStages / 2)) + wg;
+      if (!mbar_wait_warp(&codes_full[stage], uint32_t(i / (kStages / 2)) & 1u, ctl, 1)) break;
       const uint8_t* c = smem + stage * Cfg::kCodeBytes + row * 128;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int st = 2 * i + h, buf = st % kSteps;
+        const int buf = 2 * wg + h;  // (kSteps = 4: two of this group's, two of the other's)
         uint4 w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           w[j] = *reinterpret_cast<const uint4*>(c + (((h * 4 + j) ^ (row & 7)) << 4));
-        ok = mbar_wait_warp(&step_free[buf], (uint32_t(st / kSteps) & 1u) ^ 1u, ctl, 2);
+        ok = mbar_wait_warp(&step_free[buf], (uint32_t(i) & 1u) ^ 1u, ctl, 2);
         if (!ok) break;
         tc_fence_after();
         const uint32_t dst = tmem_addr(tmem, quad * 32, Cfg::kUnpackedCol + buf * 64);
@@ -501,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     constexpr int kUG = Cfg::kUnitGroups;
     {
       // this warp's 16 rows of scales (the other group's warp has the rest)
-      const int pieces = half / kGroup / 8;  // 16-byte pieces of a row
+      constexpr int pieces = half / kGroup / 8;  // 16-byte pieces of a row
       const int r0 = quad * 32 + wg * 16;
       for (int i = lane; i < 16 * pieces; i += 32) {
         const int r = r0 + i / pieces, c = i % pieces;
@@ -514,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
     float acc[NT] = {};
     bool ok = true;
-    const int blocks = half / kGroup / 8;  // eight groups each
+    constexpr int blocks = half / kGroup / 8;  // eight groups each
     int use = 0;                           // units this warp has taken
     for (int b = 0; b < blocks && ok; ++b) {
       const uint4 s4 = *reinterpret_cast<const uint4*>(scales + row * pitch + b * 16);
@@ -679,14 +684,14 @@ cudaError_t launch_tc(const void* A, const void* q, const void* scale, void* C, 
   if (e != cudaSuccess) return e;
   const dim3 grid(unsigned(N / kTcRows) * 2, unsigned((M + NT - 1) / NT));
   kern<<<grid, kTcThreads, bytes, stream>>>(tmX, tmQ, static_cast<const __nv_bfloat16*>(scale),
-                                            static_cast<__nv_bfloat16*>(C), M, N, K, wait_limit_ns,
+                                            static_cast<__nv_bfloat16*>(C), M, N, wait_limit_ns,
                                             err_word, test_stall);
   return cudaGetLastError();
 }
 
 // Up to 8 tokens the streams of the first kernel (M = 8: 16.4, 17.1 and 16.0 us
-// with groups of 32, 64 and 128; the tensor-core kernel 20.8, 19.5 and 19.1); from
-// 9 on the other (M = 16: 21.2, 19.7 and 19.1 us against 25.0, 23.9 and 22.8 for
+// with groups of 32, 64 and 128; the tensor-core kernel 19.8, 18.7 and 18.1); from
+// 9 on the other (M = 16: 19.9, 18.6 and 18.1 us against 25.0, 23.9 and 22.8 for
 // streams of 16 tokens), in passes of equal width, 64 tokens at most.
 template <int kGroup>
 cudaError_t launch_group(const void* A, const void* q, const void* scale, void* C, int64_t M, int N,
