@@ -455,7 +455,10 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // complete on the even CTA's barriers.
 // Rows behind the request's last key are zeroed in the V blocks of the last
 // 64-key chunk (0 * NaN is NaN): those two blocks complete on a barrier of
-// their own CTA, a warp zeroes the rows and then reports the bytes to the ring.
+// their own CTA, a warp zeroes the rows of both and then reports the bytes to the
+// ring. (What it wrote is read by its own CTA's tensor core, so this too orders at
+// CTA scope: block by block and with fences at cluster scope it held an item's
+// last products up by 4 us.)
 //
 // Instructions are the scarce resource: eight roles share one instruction
 // cache, and with unrolled blocks and waits inline (250 KB of code) the kernel
@@ -613,10 +616,6 @@ __device__ __forceinline__ void commit_pair_el(uint32_t bar, uint32_t el) {
 __device__ __forceinline__ void arrive_even(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
                : "memory");
-}
-
-__device__ __forceinline__ void fence_acq_rel_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t mask_window(const uint32_t* mask, int words, int d) {
@@ -863,7 +862,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       bool ok = true, any = false;
       for (int g = 0; ok && walk.next(); ++g) {
         const bool first = walk.first();
-        const int cut = walk.cut();
         ok = wait_warp(&p_full[0], uint32_t(g) & 1u, waits, 7);
         if (first && walk.item_no > 0)
           ok = ok && wait_warp(&o_free, uint32_t(walk.item_no - 1) & 1u, waits, 8);
@@ -873,7 +871,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
           ok = ok && wait_warp(&v_full[pos.slot], pos.par, waits, 14);
           if (!ok) break;
           const int c = i >> 1, m = i & 1;
-          if (c == cut) fence_acq_rel_cluster();  // (reported by a thread of either CTA)
           tc_fence_after();
           const uint32_t d = tmem + kColO + m * 128;
           const uint64_t pd = p_desc + c * (kQBlk >> 4);
@@ -925,27 +922,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     uint32_t cuts = 0;
     for (int g = 0; ok && walk.next(); ++g) {
       const int cut = walk.cut();
-      if (cut >= 0)
-#pragma unroll 1
-        for (int m = 0; ok && m < 2; ++m) {
-          const uint32_t slot = (uint32_t(g) * kVBlocks + 2 * cut + m) % kVRing;
-          ok = wait_warp(&cut_full[m], (cuts >> 1) & 1u, waits, 13);
-          if (!ok) break;
-          uint8_t* blk = smem + kOffV + slot * kBlk;
-          for (int e = lane; e < (64 - walk.it.cut_row) * 16; e += 32) {  // 2 x 8 pieces of 16 bytes
-            const int row = walk.it.cut_row + (e >> 4);
-            *reinterpret_cast<uint4*>(blk + ((e >> 3) & 1) * 8192 + row * 128 + (e & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          fence_acq_rel_cluster();
-          __syncwarp();
-          ++cuts;
-          if (lane == 0) {
-            n_cut[2] = cuts;
-            mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
-          }
-        }
+      if (cut < 0) continue;
+      for (int m = 0; m < 2; ++m) ok = ok && wait_warp(&cut_full[m], (cuts >> 1) & 1u, waits, 13);
+      if (!ok) break;
+      const uint32_t first = (uint32_t(g) * kVBlocks + 2 * cut) % kVRing;
+      const uint32_t second = first + 1 == kVRing ? 0 : first + 1;
+      uint8_t* blk0 = smem + kOffV + first * kBlk;
+      uint8_t* blk1 = smem + kOffV + second * kBlk;
+      for (int e = lane; e < (64 - walk.it.cut_row) * 16; e += 32) {  // 2 x 8 pieces of 16 bytes
+        const int at = ((e >> 3) & 1) * 8192 + (walk.it.cut_row + (e >> 4)) * 128 + (e & 7) * 16;
+        *reinterpret_cast<uint4*>(blk0 + at) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(blk1 + at) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      cuts += 2;
+      if (lane == 0) {
+        n_cut[2] = cuts;
+        __threadfence_block();
+        mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[first]), 0), kBlk);
+        mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[second]), 0), kBlk);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax / epilogue
