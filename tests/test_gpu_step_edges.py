@@ -37,6 +37,19 @@ def test_attn_tree_pairs_in_step(cuda_device, ctx, nodes, P):
     assert torch.equal(out, c.call()), "two runs differ"
 
 
+@pytest.mark.parametrize("ctx,nodes,spare", [([77], [2], 3), ([0, 9], [0, 1], 6), ([300], [8], 0),
+                                             ([5000], [3], 1), ([40, 700], [9, 20], 3)])
+def test_attn_tree_few_rows(cuda_device, ctx, nodes, spare):
+    """The value kernel for up to 8 rows and the other one next to that limit:
+    rows behind the last request stay as they are, many pieces to join."""
+    c = Case(cuda_device, ctx, nodes, 16, seed=spare, spare=spare)
+    out = torch.full((c.N, 8192), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    c.call(out=out)
+    n = sum(nodes)
+    assert (out[n:] == 7.0).all()
+    check_rows(out[:n], c.want(), f"{ctx} {nodes}")
+
+
 # ------------------------------------------------------------------ 4-bit weights
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_w4_quantiser_ties_and_small_scales(cuda_device, group):
