@@ -25,10 +25,11 @@ namespace {
 // scale have 8-bit significands: w / scale is a tie m + 1/2 exactly or at least
 // 2^-10 away from one, so the integer nearest to w * (1 / scale) is the code
 // unless w - code * scale (exact in fp32) is half a scale, plus or minus: then it
-// is the even one of the two (about one of a thousand random weights). 35.8 us
-// for 117 MB in and 30 out (4.1 TB/s); dividing every weight took 61.5.
+// is the even one of the two (about one of a thousand random weights). 32.0 us
+// for 117 MB in and 30 out (4.6 TB/s); 33 with four CTAs to an SM or six, 35.8
+// with every lane working out its groups' scales, 61.5 with every weight divided.
 template <int kGroup>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 5)
     quant_weight_w4_kernel(const uint4* __restrict__ W, uint32_t* __restrict__ q,
                            __nv_bfloat16* __restrict__ scale) {
   constexpr int kLanes = kGroup / 8;
@@ -38,23 +39,44 @@ __global__ void __launch_bounds__(256)
   uint4 v[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] = __ldcs(W + base + k * 32 + lane);
+  float amax[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    amax[k] = m;
+  }
+  // The warp's 4 kGroups groups: a lane works out the scale and its reciprocal of
+  // one of them (lanes past their number repeat it) and the others fetch it.
+  constexpr int kGroups = 32 / kLanes;
+  const int mine = lane % (4 * kGroups), from = mine % kGroups * kLanes;
+  float am = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float x = __shfl_sync(0xffffffffu, amax[k], from);
+    if (mine / kGroups == k) am = x;
+  }
+  __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(am, 7.f));
+  if (__bfloat162float(sb) == 0.f) sb = __float2bfloat16_rn(1.f);
+  const float my_s = __bfloat162float(sb), my_r = __frcp_rn(my_s);
+  if (lane < 4 * kGroups) scale[base / kLanes + lane] = sb;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
     float x[8];
-    float amax = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[2 * e] = __uint_as_float(u[e] << 16);
       x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-      amax = fmaxf(amax, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
     }
-#pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.f));
-    if (__bfloat162float(sb) == 0.f) sb = __float2bfloat16_rn(1.f);
-    const float s = __bfloat162float(sb);
-    const float r = __frcp_rn(s), half = 0.5f * s;
+    const float s = __shfl_sync(0xffffffffu, my_s, k * kGroups + lane / kLanes);
+    const float r = __shfl_sync(0xffffffffu, my_r, k * kGroups + lane / kLanes);
+    const float half = 0.5f * s;
     bool tie = false;
     float c[8];
 #pragma unroll
@@ -90,7 +112,6 @@ __global__ void __launch_bounds__(256)
     };
     const int64_t i = base + k * 32 + lane;
     q[i] = four(c[0], c[1], c[2], c[3]) | (four(c[4], c[5], c[6], c[7]) << 16);
-    if ((lane & (kLanes - 1)) == 0) scale[i / kLanes] = sb;
   }
 }
 
