@@ -454,9 +454,13 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // forwarded the arrivals added as much to every tile). Ring copies of both CTAs
 // complete on the even CTA's barriers.
 // Rows behind the request's last key are zeroed in the V blocks of the last
-// 64-key chunk (0 * NaN is NaN): those two blocks complete on a barrier of
+// 64-key chunk (0 * NaN is NaN): those two blocks complete on barriers of
 // their own CTA, a warp zeroes the rows of both and then reports the bytes to the
-// ring. (What it wrote is read by its own CTA's tensor core, so this too orders at
+// ring. Cuts can follow one another closely (the last chunk of a tile, then the
+// first of the next: blocks 8 g + 6 and 8 g + 8, and a block is fetched as soon as
+// the third before it has been used), so a product's cuts take two barriers in
+// turn: one is armed again at the earliest for the block four on, when its last
+// block has been used and so been reported. (What it wrote is read by its own CTA's tensor core, so this too orders at
 // CTA scope: block by block and with fences at cluster scope it held an item's
 // last products up by 4 us.)
 //
@@ -666,11 +670,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
                                       // is the other warps' part of O's rescaling
   __shared__ uint64_t p_free[2];      // the value products have read P of key half h
   __shared__ uint64_t o_free;         // even CTA: both CTAs have read O of an item
-  __shared__ uint64_t cut_full[2];    // this CTA's cut V block of product m landed
+  __shared__ uint64_t cut_full[2][2];  // this CTA's cut V block of product m landed (cut n: [m][n % 2])
   __shared__ uint64_t drain_bar[2];   // the two issuers' products in flight
   __shared__ uint64_t never_bar;      // no thread ever arrives (failure-detection test)
   __shared__ uint32_t n_issued[5];    // blocks this CTA's producers issued: K (2), V (2), query
-  __shared__ uint32_t n_cut[3];       // cut blocks issued (by product), reported
+  __shared__ uint32_t n_cut[3];       // cut blocks issued (by product), cuts reported
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float xch[2][2][64];     // maxima of a row's two halves, by parity of the tile
@@ -704,7 +708,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       mbar_init(&s_free[i], 8);
       mbar_init(&p_full[i], i == 0 ? 8 : 4);
       mbar_init(&p_free[i], 1);
-      mbar_init(&cut_full[i], 1);
+      mbar_init(&cut_full[i][0], 1);
+      mbar_init(&cut_full[i][1], 1);
       mbar_init(&drain_bar[i], 1);
     }
     mbar_init(&o_free, 8);
@@ -776,7 +781,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       RingPos<kVRing> pos;
       if (odd) pos.advance();
       const uint32_t full0 = mapa_shared(smem_u32(&v_full[0]), 0);
-      const uint32_t cut0 = mapa_shared(smem_u32(&cut_full[odd]), rank);
+      const uint32_t cut0 = mapa_shared(smem_u32(&cut_full[odd][0]), rank);
       const int vi = lane & (per - 1), vj = lane >> (6 - box_shift);  // box, 64-column half
       const int col = odd * 256 + int(rank) * 128 + vj * 64;          // (block i: product m = i % 2)
       uint8_t* dst = smem + kOffV + vj * 8192 + (vi << box_shift) * 128;
@@ -797,12 +802,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
           }
           uint32_t bar = full0 + pos.slot * 8;
           if (c == cut) {
-            ++cuts;
             if (lane == 0) {
-              mbar_arrive_expect_tx(&cut_full[odd], kBlk);
-              n_cut[odd] = cuts;
+              mbar_arrive_expect_tx(&cut_full[odd][cuts & 1u], kBlk);
+              n_cut[odd] = cuts + 1;
             }
-            bar = cut0;
+            bar = cut0 + (cuts & 1u) * 8;
+            ++cuts;
           }
           if (lane < 2 * per)
             tma_load_3d_pair(dst + pos.slot * kBlk, &tmC, bar, col,
@@ -919,11 +924,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         s.row_info[n] = place_of(s, int(gridDim.x >> 1), n);
     __syncwarp();
     bool ok = true;
-    uint32_t cuts = 0;
+    uint32_t cuts = 0;  // so far, both products' blocks of one counting as one
     for (int g = 0; ok && walk.next(); ++g) {
       const int cut = walk.cut();
       if (cut < 0) continue;
-      for (int m = 0; m < 2; ++m) ok = ok && wait_warp(&cut_full[m], (cuts >> 1) & 1u, waits, 13);
+      for (int m = 0; m < 2; ++m)
+        ok = ok && wait_warp(&cut_full[m][cuts & 1u], (cuts >> 1) & 1u, waits, 13);
       if (!ok) break;
       const uint32_t first = (uint32_t(g) * kVBlocks + 2 * cut) % kVRing;
       const uint32_t second = first + 1 == kVRing ? 0 : first + 1;
@@ -936,7 +942,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      cuts += 2;
+      ++cuts;
       if (lane == 0) {
         n_cut[2] = cuts;
         __threadfence_block();
@@ -1149,18 +1155,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     int zero = 0;
     const Waits drain{&zero, err_word, wait_limit_ns};
     Walk w(a, s, int(blockIdx.x >> 1));
-    const uint32_t all = n_cut[0] + n_cut[1];
-    uint32_t item = 0;  // items with a cut so far
-    for (int g = 0; 2 * item < all && w.next(); ++g) {
+    const uint32_t all = max(n_cut[0], n_cut[1]);
+    uint32_t n = 0;  // cuts so far
+    for (int g = 0; n < all && w.next(); ++g) {
       const int cut = w.cut();
       if (cut < 0) continue;
       for (int m = 0; m < 2; ++m)
-        if (item < n_cut[m] && 2 * item + m >= n_cut[2]) {
+        if (n < n_cut[m] && n >= n_cut[2]) {
           const uint32_t slot = (uint32_t(g) * kVBlocks + 2 * cut + m) % kVRing;
-          wait_more(&cut_full[m], item & 1u, drain, 16);
+          wait_more(&cut_full[m][n & 1u], (n >> 1) & 1u, drain, 16);
           mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
         }
-      ++item;
+      ++n;
     }
   }
   __syncwarp();
