@@ -518,7 +518,7 @@ mla_status_t mla_cache_append(const mla_bf16* c_kv, const mla_bf16* k_pe,
 
 /*
  * Workspace bytes of mla_attn_tree: the status word, the schedule (6.5 KB, 32
- * bytes a request and 20 a row), the queries (bf16) and results (fp32) in latent
+ * bytes a request, 20 and a bit a row), the queries (bf16) and results (fp32) in latent
  * form (N * 64 * (576 * 2 + 512 * 4)) and 37.1 MiB of partial results. Returns 0
  * for B or N out of range.
  */

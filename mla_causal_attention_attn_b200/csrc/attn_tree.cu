@@ -77,7 +77,8 @@ struct Scratch {
   Share* share;        // [kMaxClusters]
   TreeReq* req;        // [B]
   int* row_req;        // [N]: the last request that starts at or before the row
-  int4* row_info;      // [N]: where the row's results are (RowInfo)
+  int4* row_info;      // [N]: where the row's results are (place_of)
+  uint32_t* unseen;    // [N / 32]: bit n % 32 of word n / 32: no node of row n's request sees it
   __nv_bfloat16* q;    // [N, 64, 576]
   float* o;            // [N, 64, 512], pairs in one share
   float* part_o;       // [kMaxSlots][128][512]
@@ -99,6 +100,8 @@ Scratch carve(void* base, int B, int64_t N) {
   p += up256(size_t(N) * 4);
   s.row_info = reinterpret_cast<int4*>(p);
   p += up256(size_t(N) * 16);
+  s.unseen = reinterpret_cast<uint32_t*>(p);
+  p += up256((size_t(N) + 31) / 32 * 4);
   s.q = reinterpret_cast<__nv_bfloat16*>(p);
   p += up256(size_t(N) * kHeads * kRow * 2);
   s.o = reinterpret_cast<float*>(p);
@@ -280,13 +283,32 @@ __device__ __forceinline__ void cp_wait() {
 // the next ones on their way. The CTAs of the first y row do the rest: the first
 // lays out the schedule and clears the status word, the others rotate the
 // rotary parts (a warp turns 8 heads of a token by one sine and cosine per
-// lane) and find the rows' requests.
+// lane) and find the rows' requests and those that nobody sees.
 constexpr int kQTok = 32;
 constexpr int kQThreads = 256;
 constexpr int kQCols = 128;
 constexpr int kQLd = 128 + 8;  // padded rows, in elements
 constexpr int kQHeads = 8;     // heads a warp rotates with one angle
 constexpr size_t kQSmem = size_t(kNope + 3 * kQTok) * kQLd * 2;
+
+// Whether no node of request l names row n in its mask row. Most nodes see
+// themselves; the others' columns are searched.
+__device__ __noinline__ bool is_unseen(const AttnTreeArgs& a, int l, int n) {
+  const int start = min(max(a.cu_new[l], 0), a.N);
+  const int nodes = min(a.cu_new[l + 1], a.N) - start, d = n - start;
+  if (d < 0 || d >= nodes) return false;  // not a node
+  if (d >> 5 >= a.mask_words) return true;
+  const uint32_t* col = a.tree_mask + size_t(start) * a.mask_words + (d >> 5);
+  const uint32_t bit = 1u << (d & 31);
+  if (col[size_t(d) * a.mask_words] & bit) return false;
+  for (int i = 0; i < nodes; i += 8) {
+    uint32_t any = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) any |= col[size_t(min(i + e, nodes - 1)) * a.mask_words];
+    if (any & bit) return false;
+  }
+  return true;
+}
 
 template <bool kRope>
 __device__ void rotate_queries(const AttnTreeArgs& a, const Scratch& s, const RopeFreqs& f, int part,
@@ -318,14 +340,21 @@ __device__ void rotate_queries(const AttnTreeArgs& a, const Scratch& s, const Ro
     for (int k = 0; k < kQHeads; ++k)
       reinterpret_cast<__nv_bfloat162*>(s.q + (row + k) * kRow + kLat)[lane] = y[k];
   }
-  for (int n = part * kQThreads + threadIdx.x; n < a.N; n += parts * kQThreads) {
-    int l = 0, h = a.B;
-    while (h - l > 1) {
-      const int m = (l + h) >> 1;
-      if (a.cu_new[m] <= n) l = m;
-      else h = m;
+  for (int n0 = part * kQThreads + (threadIdx.x & ~31); n0 < a.N; n0 += parts * kQThreads) {
+    const int n = n0 + lane;
+    bool unseen = false;
+    if (n < a.N) {
+      int l = 0, h = a.B;
+      while (h - l > 1) {
+        const int m = (l + h) >> 1;
+        if (a.cu_new[m] <= n) l = m;
+        else h = m;
+      }
+      s.row_req[n] = l;
+      if (a.tree_mask) unseen = is_unseen(a, l, n);
     }
-    s.row_req[n] = l;
+    const uint32_t bits = __ballot_sync(0xffffffffu, unseen);
+    if (lane == 0) s.unseen[n0 >> 5] = bits;
   }
 }
 
@@ -453,8 +482,9 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // scope held the arriving thread for about 0.7 us, and a helper thread that
 // forwarded the arrivals added as much to every tile). Ring copies of both CTAs
 // complete on the even CTA's barriers.
-// Rows behind the request's last key are zeroed in the V blocks of the last
-// 64-key chunk (0 * NaN is NaN): those two blocks complete on barriers of
+// Rows that no node sees may hold anything, and 0 * NaN is NaN: rows behind the
+// request's last key and new tokens that no mask row names are zeroed in the V
+// blocks of their 64-key chunk. Such a chunk's two blocks complete on barriers of
 // their own CTA, a warp zeroes the rows of both and then reports the bytes to the
 // ring. Cuts can follow one another closely (the last chunk of a tile, then the
 // first of the next: blocks 8 g + 6 and 8 g + 8, and a block is fetched as soon as
@@ -501,6 +531,38 @@ __device__ __noinline__ int4 place_of(const Scratch& s, int clusters, int n) {
   const int first = 2 * c0 + (share_begin(total, c0, clusters) < p0 ? 1 : 0);
   // a partial result's rows 64 .. 127 are the pair's second node
   return make_int4(pieces, first * 128 + (node & 1) * 64, c0, node & 1);
+}
+
+__device__ __forceinline__ uint32_t mask_window(const uint32_t* mask, int words, int d) {
+  // bits d .. d + 31 of the mask row (bits outside it are 0)
+  const int w = d >> 5, sh = d & 31;
+  const uint32_t lo = w >= 0 && w < words ? mask[w] : 0u;
+  const uint32_t hi = w + 1 >= 0 && w + 1 < words ? mask[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+
+// Which of keys k .. k + 31 are new tokens that no node of the request sees.
+// (Scalars, not the request: a reference would put it in local memory.)
+__device__ __forceinline__ uint32_t unseen_keys(const uint32_t* unseen, int rows, int start,
+                                                int ctx, int keys, int k) {
+  if (k + 32 <= ctx || k >= keys) return 0u;
+  const int d = k - ctx;  // > -32
+  uint32_t m = mask_window(unseen, (rows + 31) >> 5, start + d);
+  if (d < 0) m &= 0xffffffffu << -d;
+  if (keys - k < 32) m &= (1u << (keys - k)) - 1u;
+  return m;
+}
+
+// Which of the four 64-key chunks from key k on have such keys. (A whole warp.)
+__device__ __noinline__ uint32_t unseen_chunks(const uint32_t* unseen, int rows, int start, int ctx,
+                                               int keys, int k) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t m = lane < 8 ? unseen_keys(unseen, rows, start, ctx, keys, k + 32 * lane) : 0u;
+  const uint32_t b = __ballot_sync(0xffffffffu, m != 0u);
+  uint32_t chunks = 0u;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) chunks |= ((b >> (2 * c)) & 3u) != 0u ? 1u << c : 0u;
+  return chunks;
 }
 
 // What a cluster visits: the items of its share, tile by tile. Every role walks
@@ -552,8 +614,17 @@ struct Walk {
   }
   __device__ __forceinline__ bool first() const { return begins; }
   __device__ __forceinline__ bool last() const { return to_go == 0; }
-  // The tile's chunk with rows to be zeroed, or -1.
-  __device__ __forceinline__ int cut() const { return tile + 1 == it.r.tiles ? it.cut_last : -1; }
+  // The tile's chunk with rows behind the last key that have to be zeroed, or -1.
+  __device__ __forceinline__ int end_cut() const {
+    return tile + 1 == it.r.tiles ? it.cut_last : -1;
+  }
+  // A bit for every chunk of the tile with rows that have to be zeroed. (A whole warp.)
+  __device__ __forceinline__ uint32_t cuts() const {
+    uint32_t m = end_cut() >= 0 ? 1u << end_cut() : 0u;
+    if (a->tree_mask && (tile + 1) * kTileKeys > it.r.ctx)
+      m |= unseen_chunks(s->unseen, a->N, it.r.start, it.r.ctx, it.r.keys, tile * kTileKeys);
+    return m;
+  }
 };
 
 // A position in a ring: slot and parity of its pass.
@@ -620,14 +691,6 @@ __device__ __forceinline__ void commit_pair_el(uint32_t bar, uint32_t el) {
 __device__ __forceinline__ void arrive_even(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
                : "memory");
-}
-
-__device__ __forceinline__ uint32_t mask_window(const uint32_t* mask, int words, int d) {
-  // bits d .. d + 31 of the mask row (bits outside it are 0)
-  const int w = d >> 5, sh = d & 31;
-  const uint32_t lo = w >= 0 && w < words ? mask[w] : 0u;
-  const uint32_t hi = w + 1 >= 0 && w + 1 < words ? mask[w + 1] : 0u;
-  return __funnelshift_r(lo, hi, sh);
 }
 
 // Which of keys k .. k + 31 node `node` sees (pages aside).
@@ -789,7 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       while (ok && walk.next()) {
         const int tile_key = walk.tile * kTileKeys;
         const int pages = lane < 4 * per ? page_at(tile_key + (lane << box_shift)) : 0;
-        const int cut = walk.cut();
+        const uint32_t cut = walk.cuts();
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           const int page = __shfl_sync(0xffffffffu, pages, c * per + vi);
@@ -801,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
             n_issued[2 + odd] = issued;
           }
           uint32_t bar = full0 + pos.slot * 8;
-          if (c == cut) {
+          if ((cut >> c) & 1u) {
             if (lane == 0) {
               mbar_arrive_expect_tx(&cut_full[odd][cuts & 1u], kBlk);
               n_cut[odd] = cuts + 1;
@@ -926,28 +989,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     bool ok = true;
     uint32_t cuts = 0;  // so far, both products' blocks of one counting as one
     for (int g = 0; ok && walk.next(); ++g) {
-      const int cut = walk.cut();
-      if (cut < 0) continue;
-      for (int m = 0; m < 2; ++m)
-        ok = ok && wait_warp(&cut_full[m][cuts & 1u], (cuts >> 1) & 1u, waits, 13);
-      if (!ok) break;
-      const uint32_t first = (uint32_t(g) * kVBlocks + 2 * cut) % kVRing;
-      const uint32_t second = first + 1 == kVRing ? 0 : first + 1;
-      uint8_t* blk0 = smem + kOffV + first * kBlk;
-      uint8_t* blk1 = smem + kOffV + second * kBlk;
-      for (int e = lane; e < (64 - walk.it.cut_row) * 16; e += 32) {  // 2 x 8 pieces of 16 bytes
-        const int at = ((e >> 3) & 1) * 8192 + (walk.it.cut_row + (e >> 4)) * 128 + (e & 7) * 16;
-        *reinterpret_cast<uint4*>(blk0 + at) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(blk1 + at) = make_uint4(0, 0, 0, 0);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      ++cuts;
-      if (lane == 0) {
-        n_cut[2] = cuts;
-        __threadfence_block();
-        mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[first]), 0), kBlk);
-        mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[second]), 0), kBlk);
+      uint32_t cut = walk.cuts();
+#pragma unroll 1
+      for (; cut != 0u; cut &= cut - 1u) {
+        const int c = __ffs(int(cut)) - 1;
+        const int k = walk.tile * kTileKeys + 64 * c;
+        // the rows to be zeroed
+        uint32_t z0 = 0u, z1 = 0u;
+        if (a.tree_mask) {
+          const TreeReq& r = walk.it.r;
+          z0 = unseen_keys(s.unseen, a.N, r.start, r.ctx, r.keys, k);
+          z1 = unseen_keys(s.unseen, a.N, r.start, r.ctx, r.keys, k + 32);
+        }
+        if (c == walk.end_cut()) {
+          const int row = walk.it.cut_row;  // 1 .. 63
+          z0 |= row < 32 ? 0xffffffffu << row : 0u;
+          z1 |= row < 32 ? 0xffffffffu : 0xffffffffu << (row - 32);
+        }
+        for (int m = 0; m < 2; ++m)
+          ok = ok && wait_warp(&cut_full[m][cuts & 1u], (cuts >> 1) & 1u, waits, 13);
+        if (!ok) break;
+        const uint32_t first = (uint32_t(g) * kVBlocks + 2 * c) % kVRing;
+        const uint32_t second = first + 1 == kVRing ? 0 : first + 1;
+        uint8_t* blk0 = smem + kOffV + first * kBlk;
+        uint8_t* blk1 = smem + kOffV + second * kBlk;
+        for (int e = lane; e < 64 * 16; e += 32) {  // 2 x 8 pieces of 16 bytes a row
+          const int row = e >> 4;
+          if (!(((row < 32 ? z0 : z1) >> (row & 31)) & 1u)) continue;
+          const int at = ((e >> 3) & 1) * 8192 + row * 128 + (e & 7) * 16;
+          *reinterpret_cast<uint4*>(blk0 + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(blk1 + at) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        ++cuts;
+        if (lane == 0) {
+          n_cut[2] = cuts;
+          __threadfence_block();
+          mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[first]), 0), kBlk);
+          mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[second]), 0), kBlk);
+        }
       }
     }
   } else {
@@ -1149,7 +1230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
   // Without an abort every block that was issued has been read by a product.
   const bool aborted =
       abort_flag != 0 || ld_shared_cluster_u32(mapa_shared(smem_u32(&abort_flag), rank ^ 1)) != 0;
-  if (aborted && warp == 8 && lane == 0) {
+  if (aborted && warp == 8) {
     // cut blocks that were issued but not reported: they land on this CTA's
     // barriers, then count on the even CTA's
     int zero = 0;
@@ -1157,17 +1238,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     Walk w(a, s, int(blockIdx.x >> 1));
     const uint32_t all = max(n_cut[0], n_cut[1]);
     uint32_t n = 0;  // cuts so far
-    for (int g = 0; n < all && w.next(); ++g) {
-      const int cut = w.cut();
-      if (cut < 0) continue;
-      for (int m = 0; m < 2; ++m)
-        if (n < n_cut[m] && n >= n_cut[2]) {
-          const uint32_t slot = (uint32_t(g) * kVBlocks + 2 * cut + m) % kVRing;
-          wait_more(&cut_full[m][n & 1u], (n >> 1) & 1u, drain, 16);
-          mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
-        }
-      ++n;
-    }
+    for (int g = 0; n < all && w.next(); ++g)
+      for (uint32_t cut = w.cuts(); cut != 0u; cut &= cut - 1u, ++n)
+        for (int m = 0; m < 2; ++m)
+          if (lane == 0 && n < n_cut[m] && n >= n_cut[2]) {
+            const uint32_t slot =
+                (uint32_t(g) * kVBlocks + 2 * (__ffs(int(cut)) - 1) + m) % kVRing;
+            wait_more(&cut_full[m][n & 1u], (n >> 1) & 1u, drain, 16);
+            mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[slot]), 0), kBlk);
+          }
   }
   __syncwarp();
   if (aborted) cluster_sync();
@@ -1627,8 +1706,10 @@ cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, unsigned long 
 }  // namespace
 
 size_t attn_tree_scratch_bytes(int B, int64_t N) {
-  return 256 + up256(kMaxClusters * sizeof(Share)) + up256(size_t(B) * sizeof(TreeReq)) + up256(size_t(N) * 4) + up256(size_t(N) * 16) + up256(size_t(N) * kHeads * kRow * 2) +
-         up256(size_t(N) * kHeads * kLat * 4) + up256(size_t(kMaxSlots) * 128 * sizeof(float2)) +
+  return 256 + up256(kMaxClusters * sizeof(Share)) + up256(size_t(B) * sizeof(TreeReq)) +
+         up256(size_t(N) * 4) + up256(size_t(N) * 16) + up256((size_t(N) + 31) / 32 * 4) +
+         up256(size_t(N) * kHeads * kRow * 2) + up256(size_t(N) * kHeads * kLat * 4) +
+         up256(size_t(kMaxSlots) * 128 * sizeof(float2)) +
          size_t(kMaxSlots) * 128 * kLat * 4;
 }
 
