@@ -477,11 +477,15 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // maximum.
 //
 // The odd CTA's softmax warps arrive on the even CTA's barriers themselves (P
-// ready, S read, O read), with a release at CTA scope: what such an arrival
-// orders is read by the arriving CTA's own tensor core (a release at cluster
-// scope held the arriving thread for about 0.7 us, and a helper thread that
-// forwarded the arrivals added as much to every tile). Ring copies of both CTAs
-// complete on the even CTA's barriers.
+// ready, S read, O read). What they publish lies in their own CTA's shared memory,
+// so the order that the even CTA's issuing warps need is a release and an acquire
+// at cluster scope of shared memory alone: 64 requests of one row and up to 8192
+// keys take 114 us with fences of that restriction, 16 of 25 rows and up to 4096
+// keys 139 (113 and 137 with arrivals and waits at CTA scope, which promise
+// nothing between two CTAs). Unrestricted ones hold the arriving thread for about
+// 0.7 us and the waiting one for 480 clocks: 139 and 161 us, or 120 and 147 with
+// warps of the odd CTA that forward the arrivals. Ring copies of both CTAs complete
+// on the even CTA's barriers.
 // Rows that no node sees may hold anything, and 0 * NaN is NaN: rows behind the
 // request's last key and new tokens that no mask row names are zeroed in the V
 // blocks of their 64-key chunk. Such a chunk's two blocks complete on barriers of
@@ -490,9 +494,9 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // first of the next: blocks 8 g + 6 and 8 g + 8, and a block is fetched as soon as
 // the third before it has been used), so a product's cuts take two barriers in
 // turn: one is armed again at the earliest for the block four on, when its last
-// block has been used and so been reported. (What it wrote is read by its own CTA's tensor core, so this too orders at
-// CTA scope: block by block and with fences at cluster scope it held an item's
-// last products up by 4 us.)
+// block has been used and so been reported. (Both blocks of a chunk together:
+// one by one, with unrestricted fences, the zeroing held an item's last products up
+// by 4 us.)
 //
 // Instructions are the scarce resource: eight roles share one instruction
 // cache, and with unrolled blocks and waits inline (250 KB of code) the kernel
@@ -640,9 +644,8 @@ struct RingPos {
 };
 
 // The kernel's waits; a wait that does not succeed at once loops out of line.
-// They acquire at CTA scope, also where the other CTA's helper arrives: what
-// such a wait orders is read by the tensor core, behind tcgen05 fences, not by
-// the waiting thread (an acquire at cluster scope cost about 480 clocks each).
+// Where threads of the other CTA arrive, the wait is wait_pair, whose acquire
+// reaches them.
 struct Waits {
   int* abort_flag;
   unsigned int* err_word;
@@ -660,6 +663,22 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
                                           uint32_t site) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_more(bar, parity, w, site));
+}
+
+__device__ __noinline__ bool wait_more_relaxed(uint64_t* bar, uint32_t parity, const Waits w,
+                                               uint32_t site) {
+  const WaitCtl ctl{w.abort_flag, w.limit_ns, kErrKernelTree, w.err_word};
+  return mbar_wait_relaxed_cluster(bar, parity, ctl, site);
+}
+
+// Warp-uniform wait that acquires what threads of either CTA have written to
+// their shared memory before they arrived (arrive_even).
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, const Waits& w,
+                                          uint32_t site) {
+  bool ok = __all_sync(0xffffffffu, mbar_try_wait_relaxed_cluster(bar, parity));
+  if (!ok) ok = __all_sync(0xffffffffu, wait_more_relaxed(bar, parity, w, site));
+  fence_acquire_smem_cluster();
+  return ok;
 }
 
 // The pair's MMA and commit, issued by the lane with el != 0. The issuing warp
@@ -687,10 +706,15 @@ __device__ __forceinline__ void commit_pair_el(uint32_t bar, uint32_t el) {
       : "memory");
 }
 
-// Arrive on the even CTA's barrier at the offset of `bar`, release at CTA scope.
-__device__ __forceinline__ void arrive_even(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
-               : "memory");
+// Arrive on the even CTA's barrier at the offset of `bar`, releasing what this
+// thread's CTA has in shared memory to the even CTA's wait_pair.
+__device__ __forceinline__ void arrive_even(uint64_t* bar, uint32_t rank) {
+  if (rank == 0) {
+    mbar_arrive(bar);
+  } else {
+    fence_release_smem_cluster();
+    mbar_arrive_relaxed_cluster(mapa_shared(smem_u32(bar), 0));
+  }
 }
 
 // Which of keys k .. k + 31 node `node` sees (pages aside).
@@ -893,7 +917,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       for (int g = 0; ok && walk.next(); ++g) {
         const bool first = walk.first(), last = walk.last();
         const uint32_t d = tmem + kColS + 128u * uint32_t(g & 1);
-        if (g >= 2) ok = wait_warp(&s_free[g & 1], uint32_t((g >> 1) - 1) & 1u, waits, 6);
+        if (g >= 2) ok = wait_pair(&s_free[g & 1], uint32_t((g >> 1) - 1) & 1u, waits, 6);
 #pragma unroll 1
         for (int i = 0; ok && i < kKBlocks; ++i) {
           if (first) ok = wait_warp(&q_full[i], uint32_t(walk.item_no & 1), waits, 5);
@@ -930,15 +954,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       bool ok = true, any = false;
       for (int g = 0; ok && walk.next(); ++g) {
         const bool first = walk.first();
-        ok = wait_warp(&p_full[0], uint32_t(g) & 1u, waits, 7);
+        const uint32_t cut = walk.cuts();
+        ok = wait_pair(&p_full[0], uint32_t(g) & 1u, waits, 7);
         if (first && walk.item_no > 0)
-          ok = ok && wait_warp(&o_free, uint32_t(walk.item_no - 1) & 1u, waits, 8);
+          ok = ok && wait_pair(&o_free, uint32_t(walk.item_no - 1) & 1u, waits, 8);
 #pragma unroll 1
         for (int i = 0; ok && i < kVBlocks; ++i) {
-          if (i == 4) ok = wait_warp(&p_full[1], uint32_t(g) & 1u, waits, 9);
-          ok = ok && wait_warp(&v_full[pos.slot], pos.par, waits, 14);
-          if (!ok) break;
+          if (i == 4) ok = wait_pair(&p_full[1], uint32_t(g) & 1u, waits, 9);
           const int c = i >> 1, m = i & 1;
+          // (a cut block: the zeroing warps of both CTAs take part in its phase)
+          ok = ok && ((cut >> c) & 1u ? wait_pair(&v_full[pos.slot], pos.par, waits, 14)
+                                      : wait_warp(&v_full[pos.slot], pos.par, waits, 14));
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + kColO + m * 128;
           const uint64_t pd = p_desc + c * (kQBlk >> 4);
@@ -1025,7 +1052,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         ++cuts;
         if (lane == 0) {
           n_cut[2] = cuts;
-          __threadfence_block();
+          fence_release_smem_cluster();
           mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[first]), 0), kBlk);
           mbar_complete_tx_cluster(mapa_shared(smem_u32(&v_full[second]), 0), kBlk);
         }
@@ -1131,7 +1158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_even(&s_free[g & 1]);
+      if (lane == 0) arrive_even(&s_free[g & 1], rank);
       l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
       // O holds the products up to tile g - 1: rescale it once they are done.
       // Its halves of columns belong to different threads, all of one alpha
@@ -1155,7 +1182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       // The products of the first half of the keys add to all of O, so the
       // warps of the second half report their part of it before their own P.
       __syncwarp();
-      if (ok && half == 1 && lane == 0) arrive_even(&p_full[0]);
+      if (ok && half == 1 && lane == 0) arrive_even(&p_full[0], rank);
       // P goes to shared memory once the value products have read the last
       // tile's: for the first half of the keys in the middle of those products,
       // for the second half at their end, half of a tile's products before they
@@ -1173,7 +1200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
             make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (ok && lane == 0) arrive_even(&p_full[half]);
+      if (ok && lane == 0) arrive_even(&p_full[half], rank);
       if (!walk.last()) continue;
 
       // ---- epilogue of the item
@@ -1218,7 +1245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (ok && lane == 0) arrive_even(&o_free);
+      if (ok && lane == 0) arrive_even(&o_free, rank);
     }
     if (lane == 0) bulk_wait_group<0>();
   }

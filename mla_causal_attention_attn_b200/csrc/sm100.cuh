@@ -197,6 +197,66 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// Release and acquire at cluster scope of shared memory alone: orders this
+// thread's accesses to its CTA's shared memory (and those it has synchronised
+// with) before a relaxed operation that follows, and what such a release covers
+// before the accesses that follow the acquire. Unlike an unrestricted release at
+// cluster scope it does not wait for accesses to global memory.
+__device__ __forceinline__ void fence_release_smem_cluster() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+
+__device__ __forceinline__ void fence_acquire_smem_cluster() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+
+// Arrive on an mbarrier of another CTA of the cluster (address from
+// mapa_shared); orders nothing by itself.
+__device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+// Look at, and bounded wait for, a phase of a local mbarrier that threads of
+// other CTAs arrive on; fence_acquire_smem_cluster() follows a success.
+__device__ __forceinline__ bool mbar_try_wait_relaxed_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_relaxed_cluster(uint64_t* bar, uint32_t parity,
+                                                          const WaitCtl& ctl, uint32_t site) {
+  auto try_sleep = [&]() -> bool {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSleepHintNs)
+        : "memory");
+    return ok != 0;
+  };
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    if (try_sleep()) return true;
+    if (*ctl.abort_flag) return false;
+    if (globaltimer_ns() - t0 > ctl.limit_ns) {
+      *ctl.abort_flag = 1;
+      atomicCAS(ctl.err_word, 0u, kErrTimeoutFlag | ctl.kernel_code | (site & kErrSiteMask));
+      __threadfence();
+      return false;
+    }
+  }
+}
+
 // 16-byte load from another CTA's shared memory.
 __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_addr) {
   float4 v;
