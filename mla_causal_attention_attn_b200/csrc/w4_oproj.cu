@@ -628,22 +628,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       mbar_wait_warp(&drain_bar[issuer], 0, WaitCtl{&zero, wait_limit_ns, kErrKernelOprojW4, err_word}, 7);
     } else if (warp == kCodesWarp && lane == 0) {
       // ------------------------------------------------- loads
+      // Every copy has landed before the CTA leaves: another wait may give up
+      // while the last ones are on their way.
       while (loading && codes < stages) loading = next_codes();
-      if (!loading) {
-        // every copy has landed before the CTA leaves
-        int zero = 0;
-        WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
-        for (int i = codes > kStages ? codes - kStages : 0; i < codes; ++i)
-          mbar_wait(&codes_full[i % kStages], uint32_t(i / kStages) & 1u, drain, 10);
-      }
+      int zero = 0;
+      WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
+      for (int i = codes > kStages ? codes - kStages : 0; i < codes; ++i)
+        mbar_wait(&codes_full[i % kStages], uint32_t(i / kStages) & 1u, drain, 10);
     } else if (lane == 0) {
       while (loading && xs < steps) loading = next_x();
-      if (!loading) {
-        int zero = 0;
-        WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
-        for (int i = xs > kXSteps ? xs - kXSteps : 0; i < xs; ++i)
-          mbar_wait(&x_full[i % kXSteps], uint32_t(i / kXSteps) & 1u, drain, 11);
-      }
+      int zero = 0;
+      WaitCtl drain{&zero, wait_limit_ns, kErrKernelOprojW4, err_word};
+      for (int i = xs > kXSteps ? xs - kXSteps : 0; i < xs; ++i)
+        mbar_wait(&x_full[i % kXSteps], uint32_t(i / kXSteps) & 1u, drain, 11);
     }
   }
   __syncwarp();
