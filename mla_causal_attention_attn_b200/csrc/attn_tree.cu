@@ -696,14 +696,23 @@ __device__ __forceinline__ void mma_pair_el(uint32_t d, uint64_t ad, uint64_t bd
       : "memory");
 }
 
-__device__ __forceinline__ void commit_pair_el(uint32_t bar, uint32_t el) {
+__device__ __forceinline__ void commit_pair_el(uint32_t bar, uint32_t el, uint16_t ctas = 0x3) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "setp.ne.b32 q, %2, 0;\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;\n\t}" ::"r"(bar),
-      "h"(uint16_t(0x3)), "r"(el)
+      "h"(ctas), "r"(el)
       : "memory");
+}
+
+// Waits for this warp's products at the end of its role, whatever the other roles
+// did: after a wait that gave up, theirs or its own, nobody else may wait for them.
+__device__ __noinline__ void drain_products(uint64_t* bar, uint32_t el, Waits w, uint32_t site) {
+  int zero = 0;
+  w.abort_flag = &zero;
+  commit_pair_el(smem_u32(bar), el, 0x1);
+  wait_warp(bar, 0, w, site);
 }
 
 // Arrive on the even CTA's barrier at the offset of `bar`, releasing what this
@@ -913,7 +922,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem) + kOffRing, 16, 1024);
       const uint32_t empty0 = smem_u32(&k_empty[0]), q_empty0 = smem_u32(&q_empty[0]);
       RingPos<kKRing> pos;
-      bool ok = true, any = false;
+      bool ok = true;
       for (int g = 0; ok && walk.next(); ++g) {
         const bool first = walk.first(), last = walk.last();
         const uint32_t d = tmem + kColS + 128u * uint32_t(g & 1);
@@ -929,18 +938,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_pair_el(d, qd + kk * 2, kd + kk * 2, idesc, (i | kk) != 0 ? 1u : 0u, el);
-          any = true;
           commit_pair_el(empty0 + pos.slot * 8, el);
           if (last) commit_pair_el(q_empty0 + i * 8, el);
           pos.advance();
         }
         if (ok) commit_pair_el(smem_u32(&s_full[g & 1]), el);
       }
-      if (!ok && any) {
-        commit_pair_el(smem_u32(&drain_bar[0]), el);
-        int zero = 0;
-        wait_warp(&drain_bar[0], 0, Waits{&zero, err_word, wait_limit_ns}, 10);
-      }
+      drain_products(&drain_bar[0], el, Waits{nullptr, err_word, wait_limit_ns}, 10);
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ value products (even CTA)
@@ -951,7 +955,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem) + kOffV, 8192, 1024);
       const uint32_t empty0 = smem_u32(&v_empty[0]), p_free0 = smem_u32(&p_free[0]);
       RingPos<kVRing> pos;
-      bool ok = true, any = false;
+      bool ok = true;
       for (int g = 0; ok && walk.next(); ++g) {
         const bool first = walk.first();
         const uint32_t cut = walk.cuts();
@@ -974,17 +978,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             mma_pair_el(d, pd + kk * 2, vd + kk * (16 * 128 >> 4), idesc,
                         (!first || c > 0 || kk > 0) ? 1u : 0u, el);
-          any = true;
           commit_pair_el(empty0 + pos.slot * 8, el);
           if ((i & 3) == 3) commit_pair_el(p_free0 + (i >> 2) * 8, el);
           pos.advance();
         }
       }
-      if (!ok && any) {
-        commit_pair_el(smem_u32(&drain_bar[1]), el);
-        int zero = 0;
-        wait_warp(&drain_bar[1], 0, Waits{&zero, err_word, wait_limit_ns}, 18);
-      }
+      drain_products(&drain_bar[1], el, Waits{nullptr, err_word, wait_limit_ns}, 18);
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ query blocks
