@@ -652,6 +652,12 @@ struct Waits {
   unsigned long long limit_ns;
 };
 
+// A wait that spans whole tiles is given four times what they take on top.
+__device__ __forceinline__ Waits spanning(Waits w, int tiles) {
+  w.limit_ns += (unsigned long long)(tiles) * 16384u;
+  return w;
+}
+
 __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, const Waits w,
                                        uint32_t site) {
   const WaitCtl ctl{w.abort_flag, w.limit_ns, kErrKernelTree, w.err_word};
@@ -991,14 +997,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       const uint32_t full0 = mapa_shared(smem_u32(&q_full[0]), 0);
       uint32_t issued = 0;
       bool ok = true;
+      int tiles = 0;  // of the item before, which the waits span
       while (ok && walk.next()) {
         if (!walk.first()) continue;
+        const Waits longer = spanning(waits, tiles);
+        tiles = walk.to_go + 1;
         const int node = 2 * walk.it.pair + int(rank);
         const int row =
             node < walk.it.r.nodes ? (walk.it.r.start + node) * kHeads : a.N * kHeads;  // zeros
 #pragma unroll 1
         for (int i = 0; i < kKBlocks; ++i) {
-          ok = wait_more(&q_empty[i], uint32_t(walk.item_no & 1) ^ 1u, waits, 2);
+          ok = wait_more(&q_empty[i], uint32_t(walk.item_no & 1) ^ 1u, longer, 2);
           if (!ok) break;
           if (leader) mbar_arrive_expect_tx(&q_full[i], 2 * kQBlk);
           n_issued[4] = ++issued;
@@ -1014,6 +1023,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     __syncwarp();
     bool ok = true;
     uint32_t cuts = 0;  // so far, both products' blocks of one counting as one
+    int seen = 0;       // tiles up to the last cut
     for (int g = 0; ok && walk.next(); ++g) {
       uint32_t cut = walk.cuts();
 #pragma unroll 1
@@ -1032,8 +1042,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
           z0 |= row < 32 ? 0xffffffffu << row : 0u;
           z1 |= row < 32 ? 0xffffffffu : 0xffffffffu << (row - 32);
         }
+        const Waits longer = spanning(waits, g - seen);
+        seen = g;
         for (int m = 0; m < 2; ++m)
-          ok = ok && wait_warp(&cut_full[m][cuts & 1u], (cuts >> 1) & 1u, waits, 13);
+          ok = ok && wait_warp(&cut_full[m][cuts & 1u], (cuts >> 1) & 1u, longer, 13);
         if (!ok) break;
         const uint32_t first = (uint32_t(g) * kVBlocks + 2 * c) % kVRing;
         const uint32_t second = first + 1 == kVRing ? 0 : first + 1;

@@ -6,6 +6,10 @@ The ends differ in the 64-key chunk that a request's last key lies in, since the
 rows behind that key are zeroed on the way to the value products and the blocks
 that need it come in any order.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -13,6 +17,8 @@ import torch
 import step_ref as ref
 from mla_causal_attention_attn_b200 import binding
 from test_gpu_step import Case, check_rows, tree_words
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +146,48 @@ def test_unseen_nodes_of_a_replayed_step(cuda_device):
         graph.replay()
         torch.cuda.synchronize()
         check_rows(out, c.want(), "replayed")
+
+
+# ------------------------------------------------------------------ long shares, short wait limit
+LONG = r"""
+import sys
+sys.path.insert(0, ROOT); sys.path.insert(0, ROOT + "/tests")
+import torch
+from mla_causal_attention_attn_b200 import binding
+from test_gpu_step_tails import long_call
+out, status, word = long_call(torch.device("cuda:0"))
+assert status == 0, (status, hex(word))
+torch.save(out.cpu(), OUT)
+"""
+
+
+def long_call(dev):
+    """200 new tokens over 400000 cached ones (of few distinct pages): 74 clusters
+    work on one to two pairs of nodes each, 1564 tiles a pair."""
+    g = torch.Generator(device=dev).manual_seed(12)
+    P, ctx, N = 128, 400000, 200
+    n_pages = -(-(ctx + N) // P)
+
+    def rnd(*shape, std=1.0):
+        return (torch.randn(*shape, generator=g, device=dev) * std).to(torch.bfloat16)
+    cache = rnd(12, P, 576)
+    table = (torch.arange(n_pages, device=dev) * 7 % 9).to(torch.int32).view(1, -1)
+    table[0, -3:] = torch.tensor([9, 10, 11], device=dev)
+    ws = torch.empty(binding.attn_tree_workspace_bytes(1, N), dtype=torch.uint8, device=dev)
+    out = binding.attn_tree(rnd(N, 64, 128), rnd(N, 64, 64), rnd(64 * 256, 512, std=0.02), cache,
+                            table, torch.tensor([ctx], dtype=torch.int32, device=dev),
+                            torch.tensor([0, N], dtype=torch.int32, device=dev), workspace=ws)
+    return (out, *binding.last_device_status(ws))
+
+
+def test_waits_that_span_a_long_item(cuda_device, tmp_path):
+    """With a wait limit of a millisecond a call of several is not a call that
+    hangs: the waits for the end of an item, and for its last rows, span it."""
+    want, status, _ = long_call(cuda_device)
+    assert status == 0
+    path = str(tmp_path / "out.pt")
+    code = f"ROOT = {ROOT!r}\nOUT = {path!r}\n" + LONG
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=600,
+                         env=dict(os.environ, MLA_WAIT_LIMIT_NS="1000000"))
+    assert res.returncode == 0, res.stderr[-3000:]
+    assert torch.equal(torch.load(path), want.cpu())
