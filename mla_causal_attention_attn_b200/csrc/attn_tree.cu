@@ -229,15 +229,6 @@ __device__ void schedule(const AttnTreeArgs& a, const Scratch& s, int clusters) 
 }
 
 // ---------------------------------------------------------------- fragments
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -252,13 +243,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// 16-byte asynchronous copy; reads nothing and writes zeros when !valid.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-
 // Programmatic dependent launch: lets the next kernel of the call start its
 // prologue, and waits until the one before has completed and its writes are
 // visible.
@@ -267,13 +251,6 @@ __device__ __forceinline__ void launch_dependents() {
 }
 __device__ __forceinline__ void wait_for_primary() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ---------------------------------------------------------------- query
@@ -385,13 +362,13 @@ __global__ void __launch_bounds__(kQThreads)
         const int n = i / (kNope / 8), c = i % (kNope / 8) * 8;
         const int row = min(tile * kQTok + n, a.N - 1);
         cp16(smem_u32(sq0 + (buf * kQTok + n) * kQLd + c),
-             qn + (size_t(row) * kHeads + h) * kNope + c, true);
+             qn + (size_t(row) * kHeads + h) * kNope + c);
       }
     cp_commit();
   };
   for (int i = threadIdx.x; i < kNope * (kQCols / 8); i += kQThreads) {
     const int e = i / (kQCols / 8), c = i % (kQCols / 8) * 8;
-    cp16(smem_u32(sw + e * kQLd + c), w + size_t(e) * kLat + c, true);
+    cp16(smem_u32(sw + e * kQLd + c), w + size_t(e) * kLat + c);
   }
   cp_commit();
   const int first = blockIdx.y - 1;
@@ -1437,7 +1414,7 @@ __global__ void __launch_bounds__(kFewThreads)
   const auto* w = static_cast<const __nv_bfloat16*>(a.w_kv_b) + (size_t(h) * 256 + kNope + e0) * kLat;
   for (int i = tid; i < kFewDims * (kLat / 8); i += kFewThreads) {
     const int e = i / (kLat / 8), c = i % (kLat / 8) * 8;
-    cp16(smem_u32(sw + e * kVLd + c), w + size_t(e) * kLat + c, true);
+    cp16(smem_u32(sw + e * kVLd + c), w + size_t(e) * kLat + c);
   }
   cp_commit();
   wait_for_primary();  // (the weights are on their way already)
@@ -1451,13 +1428,13 @@ __global__ void __launch_bounds__(kFewThreads)
     if (j == 0) {
       const uint32_t to = smem_u32(raw + q * 128 + lane);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) cp16(to + c * 512, src + (c * 32 + lane) * 4, true);
+      for (int c = 0; c < 4; ++c) cp16(to + c * 512, src + (c * 32 + lane) * 4);
       if (r.at.x == 2) {
         r.ml0 = s.part_ml[p0];
         r.ml1 = s.part_ml[p1];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          cp16(to + kFew * kLat * 4 + c * 512, s.part_o + p1 * kLat + (c * 32 + lane) * 4, true);
+          cp16(to + kFew * kLat * 4 + c * 512, s.part_o + p1 * kLat + (c * 32 + lane) * 4);
       }
     }
   }
@@ -1608,13 +1585,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const float* src = r.at.x == 1 ? s.o + (size_t(n) * kHeads + h) * kLat : s.part_o + p0 * kLat;
         const uint32_t to = smem_u32(raw + q * 128 + lane);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) cp16(to + c * 512, src + (c * 32 + lane) * 4, true);
+        for (int c = 0; c < 4; ++c) cp16(to + c * 512, src + (c * 32 + lane) * 4);
         if (r.at.x == 2) {
           r.ml0 = s.part_ml[p0];
           r.ml1 = s.part_ml[p1];
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            cp16(to + kTTok * kLat * 4 + c * 512, s.part_o + p1 * kLat + (c * 32 + lane) * 4, true);
+            cp16(to + kTTok * kLat * 4 + c * 512, s.part_o + p1 * kLat + (c * 32 + lane) * 4);
         }
       }
     }

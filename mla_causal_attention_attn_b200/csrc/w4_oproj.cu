@@ -116,15 +116,6 @@ __global__ void __launch_bounds__(256, 5)
 }
 
 // ---------------------------------------------------------------- product
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // d = a b (a sum's first product).
 __device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                                 uint32_t b1) {
@@ -143,10 +134,6 @@ __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x) {
   const __nv_bfloat162 r = __hsub2(reinterpret_cast<const __nv_bfloat162&>(v),
                                    reinterpret_cast<const __nv_bfloat162&>(m));
   return reinterpret_cast<const uint32_t&>(r);
-}
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 constexpr int kW4Threads = 256;
@@ -191,7 +178,7 @@ __global__ void __launch_bounds__(kW4Threads)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         cp16(r0 + i * 8 * kW4Pitch + (step % kW4Ring) * 64, q0 + i * 8 * (K / 2) + step * 64);
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_commit();
   };
 #pragma unroll
   for (int i = 0; i < kW4Ring; ++i) fetch(i);
@@ -227,7 +214,7 @@ __global__ void __launch_bounds__(kW4Threads)
 #pragma unroll
       for (int e = 0; e < kPer; ++e)
         s[h][e] = __uint_as_float(e & 1 ? ss[b][h][e / 2] & 0xffff0000u : ss[b][h][e / 2] << 16);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kW4Ring - 1) : "memory");
+    cp_wait<kW4Ring - 1>();
     __syncwarp();
     const uint8_t* cw = ring + g * kW4Pitch + (step % kW4Ring) * 64 + t * 4;
     float d[4];
@@ -534,8 +521,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         cp16(smem_u32(scales + r * pitch + c * 16),
              scale + size_t(n0 + r) * (K / kGroup) + k0 / kGroup + c * 8);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      cp_commit();
+      cp_wait<0>();
       named_barrier_sync(1, 256);
     }
     float acc[NT] = {};
