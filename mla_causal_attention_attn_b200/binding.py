@@ -630,6 +630,14 @@ def _on(index, t, dtype, shape, name):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _rank(t, ndim, name):
+    """``t``'s shape, of ``ndim`` dimensions."""
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimension{'s' * (ndim > 1)}, "
+                         f"got shape {tuple(t.shape)}")
+    return t.shape
+
+
 def _cuda_device(t, name):
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -663,13 +671,13 @@ def page_plan(context_len, new_len, free_pages, block_table, page_size, num_page
     lib = _lib or load()
     dev = _cuda_device(context_len, "context_len")
     i32 = torch.int32
-    B = context_len.shape[0]
+    B = _rank(context_len, 1, "context_len")[0]
     _on(dev, context_len, i32, (B,), "context_len")
     _on(dev, new_len, i32, (B,), "new_len")
     n_free = 0 if free_pages is None else free_pages.numel()
     if n_free:
         _on(dev, free_pages, i32, (n_free,), "free_pages")
-    cols = block_table.shape[1]
+    cols = _rank(block_table, 2, "block_table")[1]
     _on(dev, block_table, i32, (B, cols), "block_table")
     if node_depth is not None:
         _on(dev, node_depth, i32, (max_tokens,), "node_depth")
@@ -710,7 +718,7 @@ def cache_append(c_kv, k_pe, slot_map, cache, positions=None, rope=None, stream=
     it as it is. Returns ``cache``."""
     lib = _lib or load()
     dev = _cuda_device(c_kv, "c_kv")
-    N = c_kv.shape[0]
+    N = _rank(c_kv, 2, "c_kv")[0]
     _on(dev, c_kv, torch.bfloat16, (N, KV_RANK), "c_kv")
     _on(dev, k_pe, torch.bfloat16, (N, DR), "k_pe")
     _on(dev, slot_map, torch.int32, (N,), "slot_map")
@@ -751,18 +759,18 @@ def attn_tree(q_nope, q_pe, W_kv_b, cache, block_table, context_len, cu_new, tre
     lib = _lib or load()
     dev = _cuda_device(q_nope, "q_nope")
     bf16, i32 = torch.bfloat16, torch.int32
-    N, B = q_nope.shape[0], context_len.shape[0]
+    N, B = _rank(q_nope, 3, "q_nope")[0], _rank(context_len, 1, "context_len")[0]
     _on(dev, q_nope, bf16, (N, H, DN), "q_nope")
     _on(dev, q_pe, bf16, (N, H, DR), "q_pe")
     _on(dev, W_kv_b, bf16, (H * (DN + DV), KV_RANK), "W_kv_b")
     n_pages, page, stride = _cache_pages(cache, dev)
-    cols = block_table.shape[1]
+    cols = _rank(block_table, 2, "block_table")[1]
     _on(dev, block_table, i32, (B, cols), "block_table")
     _on(dev, context_len, i32, (B,), "context_len")
     _on(dev, cu_new, i32, (B + 1,), "cu_new")
     words = 0
     if tree_mask is not None:
-        words = tree_mask.shape[1]
+        words = _rank(tree_mask, 2, "tree_mask")[1]
         _on(dev, tree_mask, i32, (N, words), "tree_mask")
     yr = _step_rope(rope, positions, N, dev)
     scale = _inputs.DEFAULT_SCALE if softmax_scale is None else float(softmax_scale)
@@ -823,10 +831,10 @@ def o_proj_w4(attn, W_q, W_scale, out=None, stream=None):
     group size is 8192 / W_scale's columns."""
     lib = _lib or load()
     dev = _cuda_device(attn, "attn")
-    M = attn.shape[0]
+    M = _rank(attn, 2, "attn")[0]
     _on(dev, attn, torch.bfloat16, (M, K_OPROJ), "attn")
     _on(dev, W_q, torch.uint8, (D_MODEL, K_OPROJ // 2), "W_q")
-    groups = W_scale.shape[1]
+    groups = _rank(W_scale, 2, "W_scale")[1]
     if groups not in (64, 128, 256):
         raise ValueError(f"W_scale must have 64, 128 or 256 columns, got {groups}")
     _on(dev, W_scale, torch.bfloat16, (D_MODEL, groups), "W_scale")

@@ -121,3 +121,10 @@ def test_binding_refuses_cpu_tensors(lib):
         binding.cache_append(x, x, t, x)
     with pytest.raises(TypeError):
         binding.attn_tree(x, x, x, x, t, t, t)
+
+
+def test_binding_rank_message():
+    assert binding._rank(torch.zeros(3, 4), 2, "x") == (3, 4)
+    for shape, ndim in (((), 1), ((4,), 2), ((4, 4), 1), ((2, 3, 4), 2)):
+        with pytest.raises(ValueError, match="x must have"):
+            binding._rank(torch.zeros(shape), ndim, "x")
