@@ -493,6 +493,12 @@ mla_status_t mla_attn_oproj_fp8(const mla_bf16* q_nope, const mla_bf16* q_pe,
  *                list ran out). Sums saturate at 2^31 - 1.
  *   B 1..65535, max_tokens 1..2^30, max_pages 1..2^31 - 1, n_free >= 0
  * Tokens past max_tokens are not planned (cu_new and counts still count them).
+ * After drafted tokens have been rejected the next plan begins at the new
+ * context_len: pages behind its ceil(context / page_size) are asked for anew and
+ * their entries written over, so the caller puts those entries back into its free
+ * list first. It also sees to it that the accepted tokens lie in the slots right
+ * behind the old context: for a path that is not the nodes 0, 1, 2, .. their rows
+ * have to be moved there (no call here does that).
  */
 mla_status_t mla_page_plan(const int32_t* context_len, const int32_t* new_len, int B,
                            const int32_t* free_pages, int n_free, const int32_t* node_depth,
@@ -549,7 +555,11 @@ size_t mla_attn_tree_workspace_bytes(int B, int64_t N);
  *              calls that can overlap.
  * A visible token whose table entry names no page is taken as not visible.
  * Cache rows that no node of the request sees may hold anything (NaN
- * included); rows that some node sees must be finite.
+ * included), those of new tokens that no mask row names among them; rows that
+ * some node sees must be finite.
+ * To bf16 are rounded: the queries in latent form and the rotated q_pe (as the
+ * prefill calls round k_nope and q_pe), the softmax numerators (their sum is
+ * taken before that) and the result. Everything else is fp32 or more.
  */
 mla_status_t mla_attn_tree(const mla_bf16* q_nope, const mla_bf16* q_pe, const mla_bf16* W_kv_b,
                            const int32_t* positions, const mla_yarn_rope_t* rope,
@@ -582,8 +592,9 @@ mla_status_t mla_quantize_weight_w4(const mla_bf16* W, int group, uint8_t* W_q, 
 /*
  *   attn [M, 8192] bf16, W_q and W_scale as above, group 32, 64 or 128 (else
  *   MLA_ERR_SHAPE), out [M, 7168] bf16, M 1 .. 2^20. All pointers 16-byte
- *   aligned. Meant for M up to about 128 (one reading of W_q per 64 rows);
- *   mla_o_proj is the faster product for many rows.
+ *   aligned. Meant for M up to 64 (13 to 27 us; mla_o_proj takes 28 to 32): from
+ *   65 rows on W_q is read once per 64 rows and mla_o_proj is the faster product
+ *   (65 rows: 34 us against 46, 38 and 37 with groups of 32, 64 and 128).
  */
 mla_status_t mla_o_proj_w4(const mla_bf16* attn, const uint8_t* W_q, const mla_bf16* W_scale,
                            int group, int64_t M, mla_bf16* out, mla_stream_t stream);

@@ -260,7 +260,7 @@ __device__ __forceinline__ void wait_for_primary() {
 // the next ones on their way. The CTAs of the first y row do the rest: the first
 // lays out the schedule and clears the status word, the others rotate the
 // rotary parts (a warp turns 8 heads of a token by one sine and cosine per
-// lane) and find the rows' requests and those that nobody sees.
+// lane, in double, and rounds to bf16 as the score products take it) and find the rows' requests and those that nobody sees.
 constexpr int kQTok = 32;
 constexpr int kQThreads = 256;
 constexpr int kQCols = 128;
@@ -1122,7 +1122,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         m = mt;
       }
       const float mx = m == -INFINITY ? 0.f : m;
-      // P in registers, so that the scores' buffer is free for tile g + 2 before
+      // P, rounded to bf16 as the value products take it (its sum is taken before
+      // that: with the sum of the rounded numbers the result was off by as much), in
+      // registers, so that the scores' buffer is free for tile g + 2 before
       // the value products of tile g - 1 have left P's
       uint32_t pk[64];
       float acc[4] = {0.f, 0.f, 0.f, 0.f};

@@ -5,8 +5,12 @@
 // multiplied on the tensor cores, with mma.sync from registers for up to 8 tokens
 // and with tcgen05 from tensor memory beyond; the fp32 sum of a group is scaled
 // and added in fp32, so nothing is rounded before the final bf16. The floor is
-// reading the codes once, 4.6 us; what bounds the kernels is turning 58.7 million
-// codes into operands (7 and 9 integer instructions for 8 codes, half rate).
+// reading the codes once, 4.6 us, and no kernel is near it. Turning 58.7 million
+// codes into operands (7 and 9 integer instructions for 8 codes, half rate) is 2.9
+// and 3.7 us of all SMs' integer pipes, so that is not what bounds them either:
+// one row finds the SMs at work for two thirds of a launch that is one short wave
+// (issue slots 44 %, integer pipe 52 %, DRAM 23 %), 37 rows wait for one another's
+// hand-offs (issue slots 37 %, integer pipe 29 %, tensor pipe 9 %, DRAM 10 %).
 #include "w4_oproj.h"
 
 #include <cuda_bf16.h>
@@ -26,7 +30,7 @@ namespace {
 // 2^-10 away from one, so the integer nearest to w * (1 / scale) is the code
 // unless w - code * scale (exact in fp32) is half a scale, plus or minus: then it
 // is the even one of the two (about one of a thousand random weights). 32.0 us
-// for 117 MB in and 30 out (4.6 TB/s); 33 with four CTAs to an SM or six, 35.8
+// for 117 MB in and 30 out (4.6 TB/s; issue slots 80 % busy); 33 with four CTAs to an SM or six, 35.8
 // with every lane working out its groups' scales, 61.5 with every weight divided.
 template <int kGroup>
 __global__ void __launch_bounds__(256, 5)
@@ -287,9 +291,13 @@ cudaError_t launch_stream(const void* A, const void* q, const void* scale, void*
 // to the others. The four partial sums meet in shared memory, the cluster's
 // included, in a fixed order. 37 tokens: 24.2 us with groups of 32, 20.0 of 128
 // (before the last step 24.4 and 20.1; without the unpacking 23.3 and 15.9,
-// without the adding 22.9 and 19.5, with one MMA a unit 23.0 and 19.3: all three
-// stages are close to one another).
-// Unpacking without the permutes, as pairs (j, j + 4), would want x permuted too.
+// without the adding 22.9 and 19.5, with one MMA a unit 23.0 and 19.3). None of
+// the three stages saves much, so with groups of 32 none of them is the limit: what
+// is left is the chain of a unit, store to tensor memory, arrive, wait, MMAs,
+// commit, wait, load, arrive, which two slots of sums (48 and 64 tokens with groups
+// of 32 or 64) can hardly cover, and 112 CTAs on 148 SMs.
+// Unpacking without the permutes, as pairs (j, j + 4), would want the codes in
+// another order in W_q, or x permuted.
 constexpr int kTcThreads = 640;  // 8 warps unpack, 8 scale and add, 2 issue MMAs, 2 load
 // 640 threads get 96 registers each; the warpgroups share them out:
 // 2 x 128 x 80 + 2 x 128 x 136 + 128 x 48 = 640 x 96.
@@ -697,7 +705,8 @@ cudaError_t launch_tc(const void* A, const void* q, const void* scale, void* C, 
 // Up to 8 tokens the streams of the first kernel (M = 8: 16.4, 17.1 and 16.0 us
 // with groups of 32, 64 and 128; the tensor-core kernel 19.8, 18.7 and 18.1); from
 // 9 on the other (M = 16: 19.9, 18.6 and 18.1 us against 25.0, 23.9 and 22.8 for
-// streams of 16 tokens), in passes of equal width, 64 tokens at most.
+// streams of 16 tokens), in passes of equal width, 64 tokens at most. (From 65 on,
+// two passes, the bf16 product is faster: 34 us against 46, 38 and 37.)
 template <int kGroup>
 cudaError_t launch_group(const void* A, const void* q, const void* scale, void* C, int64_t M, int N,
                          int K, unsigned long long wait_limit_ns, unsigned int* err_word,
