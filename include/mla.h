@@ -525,7 +525,7 @@ mla_status_t mla_cache_append(const mla_bf16* c_kv, const mla_bf16* k_pe,
 /*
  * Workspace bytes of mla_attn_tree: the status word, the schedule (6.5 KB, 32
  * bytes a request, 20 and a bit a row), the queries (bf16) and results (fp32) in latent
- * form (N * 64 * (576 * 2 + 512 * 4)) and 37.1 MiB of partial results. Returns 0
+ * form (N * 64 * (640 * 2 + 512 * 4)) and 37.1 MiB of partial results. Returns 0
  * for B or N out of range.
  */
 size_t mla_attn_tree_workspace_bytes(int B, int64_t N);
@@ -557,9 +557,9 @@ size_t mla_attn_tree_workspace_bytes(int B, int64_t N);
  * Cache rows that no node of the request sees may hold anything (NaN
  * included), those of new tokens that no mask row names among them; rows that
  * some node sees must be finite.
- * To bf16 are rounded: the queries in latent form and the rotated q_pe (as the
- * prefill calls round k_nope and q_pe), the softmax numerators (their sum is
- * taken before that) and the result. Everything else is fp32 or more.
+ * To bf16 are rounded: the queries in latent form (as the prefill calls round
+ * k_nope), the softmax numerators (their sum is taken before that) and the result.
+ * A rotated q_pe is kept as two bf16 numbers, everything else in fp32 or more.
  */
 mla_status_t mla_attn_tree(const mla_bf16* q_nope, const mla_bf16* q_pe, const mla_bf16* W_kv_b,
                            const int32_t* positions, const mla_yarn_rope_t* rope,

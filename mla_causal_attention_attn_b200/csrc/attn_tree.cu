@@ -6,9 +6,10 @@
 //   q_nope . (U_h c) = (U_h^T q_nope) . c     and     sum_j p_j V_h c_j = V_h sum_j p_j c_j,
 // so the cache is read as it lies and the per-head keys and values are never
 // formed. Three launches:
-//   1. query: q~[n, h, :] = (U_h^T q_nope[n, h], q_pe[n, h] rotated), rounded
-//      to bf16 as the operand of the score products (the same rounding that
-//      k_nope gets on the per-head path); one more CTA lays out the schedule;
+//   1. query: q~[n, h, :] = (U_h^T q_nope[n, h], q_pe[n, h] rotated) as the
+//      operand of the score products: the latent part rounded to bf16 (the same
+//      rounding that k_nope gets on the per-head path), the rotated one as two
+//      bf16 numbers; one more CTA lays out the schedule;
 //   2. attention: per item (two nodes of a request x a range of key tiles),
 //      o~ = sum_j p_j c_j with an online softmax in fp32;
 //   3. value: joins the ranges of a split request and multiplies by V_h.
@@ -30,6 +31,7 @@ constexpr int kHeads = 64;
 constexpr int kNope = 128;
 constexpr int kLat = 512;   // latent
 constexpr int kRow = 576;   // latent + rotary
+constexpr int kQRow = 640;  // a query: latent, rotary, what bf16 leaves of the rotary part
 constexpr int kVal = 128;
 constexpr int kTileKeys = 256;
 constexpr int kMaxClusters = 74;               // two SMs each
@@ -79,7 +81,7 @@ struct Scratch {
   int* row_req;        // [N]: the last request that starts at or before the row
   int4* row_info;      // [N]: where the row's results are (place_of)
   uint32_t* unseen;    // [N / 32]: bit n % 32 of word n / 32: no node of row n's request sees it
-  __nv_bfloat16* q;    // [N, 64, 576]
+  __nv_bfloat16* q;    // [N, 64, 640]; the last 64 with a rotation only
   float* o;            // [N, 64, 512], pairs in one share
   float* part_o;       // [kMaxSlots][128][512]
   float2* part_ml;     // [kMaxSlots][128] running maximum (log2 units) and sum
@@ -103,7 +105,7 @@ Scratch carve(void* base, int B, int64_t N) {
   s.unseen = reinterpret_cast<uint32_t*>(p);
   p += up256((size_t(N) + 31) / 32 * 4);
   s.q = reinterpret_cast<__nv_bfloat16*>(p);
-  p += up256(size_t(N) * kHeads * kRow * 2);
+  p += up256(size_t(N) * kHeads * kQRow * 2);
   s.o = reinterpret_cast<float*>(p);
   p += up256(size_t(N) * kHeads * kLat * 4);
   s.part_ml = reinterpret_cast<float2*>(p);
@@ -260,7 +262,7 @@ __device__ __forceinline__ void wait_for_primary() {
 // the next ones on their way. The CTAs of the first y row do the rest: the first
 // lays out the schedule and clears the status word, the others rotate the
 // rotary parts (a warp turns 8 heads of a token by one sine and cosine per
-// lane, in double, and rounds to bf16 as the score products take it) and find the rows' requests and those that nobody sees.
+// lane, in double) and find the rows' requests and those that nobody sees.
 constexpr int kQTok = 32;
 constexpr int kQThreads = 256;
 constexpr int kQCols = 128;
@@ -298,7 +300,7 @@ __device__ void rotate_queries(const AttnTreeArgs& a, const Scratch& s, const Ro
        i += int64_t(parts) * warps) {
     const int64_t n = i / (kHeads / kQHeads);
     const int64_t row = n * kHeads + i % (kHeads / kQHeads) * kQHeads;
-    __nv_bfloat162 y[kQHeads];
+    __nv_bfloat162 y[kQHeads], z[kQHeads];
 #pragma unroll
     for (int k = 0; k < kQHeads; ++k) y[k] = qp[(row + k) * kRopePairs + lane];
     if (kRope) {
@@ -309,13 +311,18 @@ __device__ void rotate_queries(const AttnTreeArgs& a, const Scratch& s, const Ro
 #pragma unroll
       for (int k = 0; k < kQHeads; ++k) {
         const double u = __bfloat162float(y[k].x), v = __bfloat162float(y[k].y);
-        y[k].x = __double2bfloat16(u * cs - v * sn);
-        y[k].y = __double2bfloat16(v * cs + u * sn);
+        const double x0 = u * cs - v * sn, x1 = v * cs + u * sn;
+        y[k] = __nv_bfloat162(__double2bfloat16(x0), __double2bfloat16(x1));
+        z[k] = __nv_bfloat162(__double2bfloat16(x0 - double(__bfloat162float(y[k].x))),
+                              __double2bfloat16(x1 - double(__bfloat162float(y[k].y))));
       }
     }
 #pragma unroll
-    for (int k = 0; k < kQHeads; ++k)
-      reinterpret_cast<__nv_bfloat162*>(s.q + (row + k) * kRow + kLat)[lane] = y[k];
+    for (int k = 0; k < kQHeads; ++k) {
+      auto* to = reinterpret_cast<__nv_bfloat162*>(s.q + (row + k) * kQRow + kLat);
+      to[lane] = y[k];
+      if (kRope) to[kRopePairs + lane] = z[k];
+    }
   }
   for (int n0 = part * kQThreads + (threadIdx.x & ~31); n0 < a.N; n0 += parts * kQThreads) {
     const int n = n0 + lane;
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__(kQThreads)
     for (int i = threadIdx.x; i < kQTok * (kQCols / 8); i += kQThreads) {
       const int n = i / (kQCols / 8), c = i % (kQCols / 8) * 8;
       if (tile * kQTok + n < a.N)
-        *reinterpret_cast<uint4*>(s.q + (size_t(tile * kQTok + n) * kHeads + h) * kRow + c0 + c) =
+        *reinterpret_cast<uint4*>(s.q + (size_t(tile * kQTok + n) * kHeads + h) * kQRow + c0 + c) =
             *reinterpret_cast<const uint4*>(sq + n * kQLd + c);
     }
     __syncthreads();  // the buffer is loaded again
@@ -433,7 +440,8 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // Two SMs per item. A cluster of two CTAs takes two nodes of a request, 64
 // rows (heads) each, so every product is one tcgen05.mma.cta_group::2 of 128
 // rows, CTA r holding node r's 64 rows and half of the other operand:
-//   S (128 x 256 keys, K = 576): each CTA holds 128 of the 256 keys;
+//   S (128 x 256 keys, K = 576, 640 with a rotation): each CTA holds 128 of the
+//     256 keys;
 //   O (128 x 512, K = 256 keys), as two products of 256 latent columns: each
 //     CTA holds 128 columns of each, of all 256 keys.
 // The accumulators of a 128-row pair product lie in tensor memory with the
@@ -475,6 +483,15 @@ __device__ __forceinline__ int page_of(const AttnTreeArgs& a, int b, int j) {
 // one by one, with unrestricted fences, the zeroing held an item's last products up
 // by 4 us.)
 //
+// With a rotation the rotary keys are multiplied twice, by q_pe rounded to bf16 and
+// by what that leaves: one rounding there is an error of the scores that grows with
+// them (scores of standard deviation 0.7, 1.4 and 2.8: the result was 0.0025, 0.0029
+// and 0.0034 to 0.0039 of its norm off, and is 0.0024, 0.0024 and 0.0025; 0.0017 is
+// its own rounding). It costs 4 MMAs in 68: 16 x 25 rows 138 -> 144 us, one row 24.1
+// -> 25.0, 64 x 1 113.7 -> 114.2. The latent part's roundings are spread over 512
+// terms of a smaller sum and would take another 32 MMAs. A kernel for each case: with
+// the number of blocks a variable calls without a rotation lost 8 %.
+//
 // Instructions are the scarce resource: eight roles share one instruction
 // cache, and with unrolled blocks and waits inline (250 KB of code) the kernel
 // ran at a tenth of its speed from cache misses. So loops over blocks stay
@@ -488,11 +505,12 @@ constexpr int kKRing = 4, kVRing = 3;
 constexpr int kKBlocks = kRow / 64;              // 9 K blocks a tile
 constexpr int kVBlocks = 8;                      // 4 chunks of 64 keys x 2 products
 constexpr uint32_t kQBlk = 64 * 128;             // one 64-dim block of a node's query rows
-constexpr uint32_t kOffP = kKBlocks * kQBlk;     // P: 4 chunks of [64 rows][64 keys]
+constexpr int kQBlocks = kQRow / 64;             // query blocks: 10 with a rotation, else 9
+constexpr uint32_t kOffP = kQBlocks * kQBlk;     // P: 4 chunks of [64 rows][64 keys]
 constexpr uint32_t kOffRing = kOffP + 4 * kQBlk;
 constexpr uint32_t kOffV = kOffRing + kKRing * kBlk;
 constexpr size_t kASmem = kOffV + kVRing * kBlk + 1024;
-static_assert(kASmem <= 225 * 1024, "shared memory budget");
+static_assert(kASmem <= 225 * 1024, "shared memory budget (227 KB with the barriers)");
 constexpr uint32_t kColO = 0, kColS = 256;       // tensor memory columns
 constexpr float kRescale = 8.f;                  // log2 growth of the maximum that rescales O
 
@@ -728,6 +746,7 @@ __device__ __forceinline__ uint32_t seen_keys(const AttnTreeArgs& a, const TreeR
   return live & (ctx_bits | (nodes & ~ctx_bits));
 }
 
+template <bool kRope>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmC,
@@ -736,13 +755,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
                      const __grid_constant__ AttnTreeArgs a,
                      const __grid_constant__ Scratch s, float scale_log2,
                      unsigned long long wait_limit_ns, unsigned int* err_word, int test_stall) {
+  constexpr int q_blocks = kRope ? kQBlocks : kKBlocks;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[kKRing];   // even CTA: both CTAs' halves of a block landed
   __shared__ uint64_t k_empty[kKRing];  // this CTA's block is free
   __shared__ uint64_t v_full[kVRing];
   __shared__ uint64_t v_empty[kVRing];
-  __shared__ uint64_t q_full[kKBlocks];   // even CTA: both CTAs' query blocks landed
-  __shared__ uint64_t q_empty[kKBlocks];  // the item's last score product has read the block
+  __shared__ uint64_t q_full[kQBlocks];   // even CTA: both CTAs' query blocks landed
+  __shared__ uint64_t q_empty[kQBlocks];  // the item's last score product has read the block
   __shared__ uint64_t s_full[2];      // scores are in buffer b
   __shared__ uint64_t s_free[2];      // even CTA: both CTAs have read buffer b
   __shared__ uint64_t p_full[2];      // even CTA: P of key half h of both CTAs is there; [0]: so
@@ -778,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < kKBlocks; ++i) {
+    for (int i = 0; i < kQBlocks; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
@@ -911,9 +931,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         const uint32_t d = tmem + kColS + 128u * uint32_t(g & 1);
         if (g >= 2) ok = wait_pair(&s_free[g & 1], uint32_t((g >> 1) - 1) & 1u, waits, 6);
 #pragma unroll 1
-        for (int i = 0; ok && i < kKBlocks; ++i) {
+        for (int i = 0; ok && i < q_blocks; ++i) {
           if (first) ok = wait_warp(&q_full[i], uint32_t(walk.item_no & 1), waits, 5);
-          ok = ok && wait_warp(&k_full[pos.slot], pos.par, waits, 4);
+          if (i < kKBlocks) ok = ok && wait_warp(&k_full[pos.slot], pos.par, waits, 4);
           if (!ok) break;
           tc_fence_after();
           const uint64_t qd = q_desc + i * (kQBlk >> 4);
@@ -921,8 +941,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_pair_el(d, qd + kk * 2, kd + kk * 2, idesc, (i | kk) != 0 ? 1u : 0u, el);
-          commit_pair_el(empty0 + pos.slot * 8, el);
           if (last) commit_pair_el(q_empty0 + i * 8, el);
+          if (i == kKBlocks - 1 && q_blocks > kKBlocks) continue;  // the rotary keys once more
+          commit_pair_el(empty0 + pos.slot * 8, el);
           pos.advance();
         }
         if (ok) commit_pair_el(smem_u32(&s_full[g & 1]), el);
@@ -983,7 +1004,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
         const int row =
             node < walk.it.r.nodes ? (walk.it.r.start + node) * kHeads : a.N * kHeads;  // zeros
 #pragma unroll 1
-        for (int i = 0; i < kKBlocks; ++i) {
+        for (int i = 0; i < q_blocks; ++i) {
           ok = wait_more(&q_empty[i], uint32_t(walk.item_no & 1) ^ 1u, longer, 2);
           if (!ok) break;
           if (leader) mbar_arrive_expect_tx(&q_full[i], 2 * kQBlk);
@@ -1276,7 +1297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
     for (int pass = 0; pass < 2; ++pass)
       for (int which = 0; which < 5; ++which) {
         uint64_t* bars = which < 2 ? k_full : which < 4 ? v_full : q_full;
-        const uint32_t ring = which < 2 ? kKRing : which < 4 ? kVRing : kKBlocks;
+        const uint32_t ring = which < 2 ? kKRing : which < 4 ? kVRing : uint32_t(q_blocks);
         const uint32_t bytes = which == 4 ? kQBlk : kBlk;
         const uint32_t stride = which == 4 ? 1 : 2, off = which == 4 ? 0 : which & 1;
         const uint32_t own = n_issued[which];
@@ -1725,7 +1746,7 @@ cudaError_t launch_value(const AttnTreeArgs& a, const Scratch& s, unsigned long 
 size_t attn_tree_scratch_bytes(int B, int64_t N) {
   return 256 + up256(kMaxClusters * sizeof(Share)) + up256(size_t(B) * sizeof(TreeReq)) +
          up256(size_t(N) * 4) + up256(size_t(N) * 16) + up256((size_t(N) + 31) / 32 * 4) +
-         up256(size_t(N) * kHeads * kRow * 2) + up256(size_t(N) * kHeads * kLat * 4) +
+         up256(size_t(N) * kHeads * kQRow * 2) + up256(size_t(N) * kHeads * kLat * 4) +
          up256(size_t(kMaxSlots) * 128 * sizeof(float2)) +
          size_t(kMaxSlots) * 128 * kLat * 4;
 }
@@ -1737,8 +1758,8 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   const int clusters = num_sms / 2 < kMaxClusters ? num_sms / 2 : kMaxClusters;
   const int box_rows = a.page_shift >= 6 ? 64 : 1 << a.page_shift;
   CUtensorMap tmQ, tmC, tmO, tmPart;
-  const uint64_t q_dims[2] = {kRow, uint64_t(a.N) * kHeads};
-  const uint64_t q_strides[1] = {kRow * 2};
+  const uint64_t q_dims[2] = {kQRow, uint64_t(a.N) * kHeads};
+  const uint64_t q_strides[1] = {kQRow * 2};
   const uint32_t q_box[2] = {64, kHeads};
   const uint64_t c_dims[3] = {kRow, uint64_t(1) << a.page_shift, uint64_t(a.num_pages)};
   const uint64_t c_strides[2] = {kRow * 2, uint64_t(a.page_stride) * 2};
@@ -1771,10 +1792,11 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, const RopeFreqs* rotary, voi
   if (e != cudaSuccess) return e;
   float scale_log2 = a.scale * 1.4426950408889634f;
   if (scale_log2 == 0.f) scale_log2 = std::numeric_limits<float>::min();  // see `hidden`
-  static ContextCache attn_attr;
-  e = ensure_smem_attr(reinterpret_cast<const void*>(tree_attn_kernel), int(kASmem), &attn_attr);
+  static ContextCache attn_attr[2];
+  auto attn = rotary ? tree_attn_kernel<true> : tree_attn_kernel<false>;
+  e = ensure_smem_attr(reinterpret_cast<const void*>(attn), int(kASmem), &attn_attr[rotary ? 1 : 0]);
   if (e != cudaSuccess) return e;
-  e = launch_after(tree_attn_kernel, dim3(2 * clusters), kAThreads, kASmem, stream, tmQ, tmC, tmO,
+  e = launch_after(attn, dim3(2 * clusters), kAThreads, kASmem, stream, tmQ, tmC, tmO,
                    tmPart, a, s, scale_log2, wait_limit_ns, err_word, test_stall);
   if (e != cudaSuccess) return e;
   return launch_value(a, s, wait_limit_ns, err_word, stream);
