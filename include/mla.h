@@ -48,7 +48,8 @@
  *    scratch. Cached per device and context: the SM count, device addresses
  *    of the library's module variables, kernel attributes.
  *  - Environment (each read once per process): MLA_WAIT_LIMIT_NS sets the
- *    bounded waits' limit in nanoseconds; MLA_ATTN_KERNEL selects the
+ *    bounded waits' limit in nanoseconds (mla_attn_tree adds 16 us for every key
+ *    tile that a wait spans); MLA_ATTN_KERNEL selects the
  *    attention kernel: unset, the one-SM kernel with 64-key score halves
  *    (under an explicit mask, 128-key tiles for the CTAs whose query tiles
  *    skip a key tile before a used one);
