@@ -649,7 +649,8 @@ struct Waits {
 
 // A wait that spans whole tiles is given four times what they take on top.
 __device__ __forceinline__ Waits spanning(Waits w, int tiles) {
-  w.limit_ns += (unsigned long long)(tiles) * 16384u;
+  const unsigned long long limit = w.limit_ns + (unsigned long long)(tiles) * 16384u;
+  if (limit > w.limit_ns) w.limit_ns = limit;  // (any 64-bit limit may be set)
   return w;
 }
 
